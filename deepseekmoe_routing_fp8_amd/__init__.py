@@ -35,6 +35,10 @@ ENTRY_POINTS = (
     "moe_unpermute_sum", "moe_transpose_fp8_blocks", "moe_grouped_ffn_fp8_backward",
     "moe_grouped_ffn_backward_workspace_bytes", "moe_grouped_ffn_intermediate_offsets",
     "moe_grouped_ffn_fp8_noalloc", "moe_grouped_ffn_fp8_gate_up_train",
+    "moe_latent_cache_row_bytes", "moe_latent_cache_write", "moe_latent_cache_read",
+    "moe_latent_attn_absorbed", "moe_latent_attn_absorbed_workspace_bytes",
+    "moe_latent_attn_expanded", "moe_latent_attn_expanded_backward",
+    "moe_latent_attn_expanded_backward_workspace_bytes",
 )
 MOE_ERR_SCRATCH = 7
 NOALLOC_SCRATCH_BYTES = 32 << 20   # MOE_NOALLOC_SCRATCH_BYTES
@@ -62,8 +66,28 @@ def make_config(cfg, scale_mode: int = SCALE_FP32) -> moe_config:
                       cfg.expert_bias_update_rate, scale_mode)
 
 
+class moe_latent_config(ctypes.Structure):
+    _fields_ = [
+        ("n_heads", ctypes.c_int32), ("latent", ctypes.c_int32), ("rope", ctypes.c_int32),
+        ("nope", ctypes.c_int32), ("v_dim", ctypes.c_int32), ("cache_kind", ctypes.c_int32),
+    ]
+
+
+MOE_CACHE_BF16, MOE_CACHE_FP8 = 0, 1
+
+
+def make_latent_config(n_heads: int, latent: int = 512, rope: int = 64, nope: int = 128,
+                       v_dim: int = 128, cache: str = "fp8") -> moe_latent_config:
+    """moe_latent_config of a latent-attention layer; ``cache``: "fp8" (E4M3 codes with a
+    power-of-two scale per 128 values) or "bf16"."""
+    kinds = {"bf16": MOE_CACHE_BF16, "fp8": MOE_CACHE_FP8}
+    if cache not in kinds:
+        raise MoEError(f"unknown cache kind {cache!r}")
+    return moe_latent_config(n_heads, latent, rope, nope, v_dim, kinds[cache])
+
+
 _P, _I64, _I32, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
-_CFG = ctypes.POINTER(moe_config)
+_CFG, _LCFG = ctypes.POINTER(moe_config), ctypes.POINTER(moe_latent_config)
 _sig = {
     "moe_status_string": ([ctypes.c_int], ctypes.c_char_p),
     "moe_quantize_1x128": ([_P, ctypes.c_int, _I64, _I64, _P, _P, _P], ctypes.c_int),
@@ -105,6 +129,17 @@ _sig = {
     "moe_grouped_ffn_fp8_backward": ([_CFG, _I32, _I64, _I64, _P, _P, _P, ctypes.c_int, _P, _P, _P,
                                       _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_int,
                                       _P, _P, _P, ctypes.c_int, _P, _SZ, _P], ctypes.c_int),
+    "moe_latent_cache_row_bytes": ([_LCFG], _SZ),
+    "moe_latent_cache_write": ([_LCFG, _I64, _P, ctypes.c_int, _I64, _P, _P, _I64, _P], ctypes.c_int),
+    "moe_latent_cache_read": ([_LCFG, _P, _I64, _I32, _P, _I64, _I64, _P, _P, _I64, _P, _P], ctypes.c_int),
+    "moe_latent_attn_absorbed_workspace_bytes": ([_LCFG, _I64, _I32], _SZ),
+    "moe_latent_attn_absorbed": ([_LCFG, _I64, _I32, _P, _P, _I64, _I32, _P, _I64, _P, ctypes.c_float, _P,
+                                  ctypes.c_int, _P, _P, _SZ, _P], ctypes.c_int),
+    "moe_latent_attn_expanded": ([_LCFG, _I64, _I64, _I64, _P, _P, _P, _P, _P, ctypes.c_float, _I32, _P,
+                                  ctypes.c_int, _P, _P], ctypes.c_int),
+    "moe_latent_attn_expanded_backward_workspace_bytes": ([_LCFG, _I64, _I64], _SZ),
+    "moe_latent_attn_expanded_backward": ([_LCFG, _I64, _I64, _I64, _P, _P, _P, _P, _P, ctypes.c_float, _I32,
+                                           _P, _P, _P, _P, _P, _P, ctypes.c_int, _P, _SZ, _P], ctypes.c_int),
 }
 for _name, (_args, _res) in _sig.items():
     _f = getattr(_lib, _name)
@@ -590,6 +625,178 @@ def moe_grouped_ffn_fp8_backward(cfg: moe_config, n_experts: int, xq, xs, x, row
         _dev(dw2, dw1.dtype, "dw2", (E, H, I)), _dt(dw1), _dev(ws, torch.uint8, "ws"), ws.numel(),
         _stream(stream)), "moe_grouped_ffn_fp8_backward")
     return dx_rows, dw1, dw3, dw2
+
+
+# ---------------------------------------------------------------------------------------
+# Latent attention
+# ---------------------------------------------------------------------------------------
+def _same_device(*tensors):
+    """The tensors' device; they have to share it, and it has to be the current one (the
+    library launches there)."""
+    dev = tensors[0].device
+    for t in tensors[1:]:
+        if t is not None and t.device != dev:
+            raise MoEError(f"tensors on different devices: {dev} and {t.device}")
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise MoEError(f"tensors on {dev}, which is not the current device")
+    return dev
+
+
+def _new(shape, dtype, dev, stream):
+    """A tensor for a call on ``stream``: memory of torch's current stream, kept until the
+    other stream is done with it."""
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _dim(t, n: int, name: str):
+    if not isinstance(t, torch.Tensor) or t.dim() != n:
+        raise MoEError(f"{name} must be a tensor of {n} dimensions")
+    return t.shape
+
+
+def moe_latent_cache_row_bytes(cfg: moe_latent_config) -> int:
+    return int(_lib.moe_latent_cache_row_bytes(ctypes.byref(cfg)))
+
+
+def _cache_args(cfg, cache):
+    """Pointer, pages and page size of a cache [n_pages, page_size, row]: uint8 rows of
+    moe_latent_cache_row_bytes bytes, or bf16 rows for a bf16 cache."""
+    n_pages, page, _ = _dim(cache, 3, "cache")
+    if cfg.cache_kind == MOE_CACHE_BF16:
+        p = _dev(cache, torch.bfloat16, "cache", (n_pages, page, cfg.latent + cfg.rope))
+    else:
+        p = _dev(cache, torch.uint8, "cache", (n_pages, page, moe_latent_cache_row_bytes(cfg)))
+    return p, n_pages, page
+
+
+def moe_latent_cache_write(cfg: moe_latent_config, x: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,
+                           stream=None) -> torch.Tensor:
+    """Writes the tokens' rows x [T, latent + rope] (bf16 or f32; rows may be strided, as a
+    slice of a wider projection is) into cache rows ``slots`` [T] int32 (page * page_size +
+    offset; negative: skipped; distinct). Returns cache."""
+    T, W = _dim(x, 2, "x")
+    _same_device(x, slots, cache)
+    if W != cfg.latent + cfg.rope:
+        raise MoEError(f"x must have {cfg.latent + cfg.rope} columns, got {W}")
+    if W > 0 and x.stride(1) != 1:
+        raise MoEError("the columns of x must be contiguous")
+    ptr, n_pages, page = _cache_args(cfg, cache)
+    _check(_lib.moe_latent_cache_write(
+        ctypes.byref(cfg), T, ctypes.c_void_p(x.data_ptr()), _xdtype(x), x.stride(0) if T > 1 else W,
+        _dev(slots, torch.int32, "slots", (T,)), ptr, n_pages * page, _stream(stream)), "moe_latent_cache_write")
+    return cache
+
+
+def moe_latent_cache_read(cfg: moe_latent_config, cache: torch.Tensor, page_table: torch.Tensor,
+                          cu_rows: torch.Tensor, starts: torch.Tensor = None, out: torch.Tensor = None,
+                          n_out: int = None, stream=None) -> torch.Tensor:
+    """-> out [n_out, latent + rope] bf16: rows cu_rows[b]..cu_rows[b+1] are sequence b's
+    positions from starts[b] (0 when None) on. Pass ``out`` or ``n_out``."""
+    B, max_pages = _dim(page_table, 2, "page_table")
+    dev = _same_device(cache, page_table, cu_rows, starts, out)
+    if out is None:
+        if n_out is None:
+            raise MoEError("pass out or n_out")
+        out = _new((n_out, cfg.latent + cfg.rope), torch.bfloat16, dev, stream)
+    ptr, n_pages, page = _cache_args(cfg, cache)
+    n = _dim(out, 2, "out")[0]
+    _check(_lib.moe_latent_cache_read(
+        ctypes.byref(cfg), ptr, n_pages, page, _dev(page_table, torch.int32, "page_table"), B, max_pages,
+        _dev(cu_rows, torch.int32, "cu_rows", (B + 1,)), _opt(starts, torch.int32, "starts", (B,)), n,
+        _dev(out, torch.bfloat16, "out", (n, cfg.latent + cfg.rope)), _stream(stream)), "moe_latent_cache_read")
+    return out
+
+
+def moe_latent_attn_absorbed_workspace_bytes(cfg: moe_latent_config, B: int, Sq: int) -> int:
+    return int(_lib.moe_latent_attn_absorbed_workspace_bytes(ctypes.byref(cfg), B, Sq))
+
+
+def moe_latent_attn_absorbed(cfg: moe_latent_config, q: torch.Tensor, cache: torch.Tensor,
+                             page_table: torch.Tensor, lengths: torch.Tensor, scale: float,
+                             out: torch.Tensor = None, lse: torch.Tensor = None, ws: torch.Tensor = None,
+                             out_dtype=torch.bfloat16, stream=None):
+    """-> (out [B, Sq, n_heads, latent], lse [B, Sq, n_heads] f32): the absorbed form for
+    q [B, Sq, n_heads, latent + rope] bf16 over the first lengths[b] cached rows of each
+    sequence, causal among the Sq tokens (whose rows the length includes)."""
+    B, Sq, H, W = _dim(q, 4, "q")
+    dev = _same_device(q, cache, page_table, lengths, out, lse, ws)
+    if out is None:
+        out = _new((B, Sq, H, cfg.latent), out_dtype, dev, stream)
+    if lse is None:
+        lse = _new((B, Sq, H), torch.float32, dev, stream)
+    if ws is None:
+        ws = _new((max(moe_latent_attn_absorbed_workspace_bytes(cfg, B, Sq), 1),), torch.uint8, dev, stream)
+    ptr, n_pages, page = _cache_args(cfg, cache)
+    max_pages = _dim(page_table, 2, "page_table")[1]
+    _check(_lib.moe_latent_attn_absorbed(
+        ctypes.byref(cfg), B, Sq, _dev(q, torch.bfloat16, "q", (B, Sq, cfg.n_heads, cfg.latent + cfg.rope)),
+        ptr, n_pages, page, _dev(page_table, torch.int32, "page_table", (B, max_pages)), max_pages,
+        _dev(lengths, torch.int32, "lengths", (B,)), scale,
+        _dev(out, out.dtype, "out", (B, Sq, H, cfg.latent)), _dt(out),
+        _dev(lse, torch.float32, "lse", (B, Sq, H)), _dev(ws, torch.uint8, "ws"), ws.numel(),
+        _stream(stream)), "moe_latent_attn_absorbed")
+    return out, lse
+
+
+def _expanded_args(cfg, q, kv, k_rope, cu_q, cu_k, scale, causal):
+    Tq, Tk, B = _dim(q, 3, "q")[0], _dim(kv, 3, "kv")[0], _dim(cu_q, 1, "cu_q")[0] - 1
+    H = cfg.n_heads
+    return (ctypes.byref(cfg), B, Tq, Tk, _dev(q, torch.bfloat16, "q", (Tq, H, cfg.nope + cfg.rope)),
+            _dev(kv, torch.bfloat16, "kv", (Tk, H, cfg.nope + cfg.v_dim)),
+            _dev(k_rope, torch.bfloat16, "k_rope", (Tk, cfg.rope)), _dev(cu_q, torch.int32, "cu_q"),
+            _dev(cu_k, torch.int32, "cu_k", (B + 1,)), scale, int(bool(causal)))
+
+
+def moe_latent_attn_expanded(cfg: moe_latent_config, q: torch.Tensor, kv: torch.Tensor, k_rope: torch.Tensor,
+                             cu_q: torch.Tensor, cu_k: torch.Tensor, scale: float, causal: bool = True,
+                             out: torch.Tensor = None, lse: torch.Tensor = None, out_dtype=torch.bfloat16,
+                             stream=None):
+    """-> (out [Tq, n_heads, v_dim], lse [n_heads, Tq] f32): the expanded form for packed
+    sequences, q [Tq, n_heads, nope + rope], kv [Tk, n_heads, nope + v_dim] (key part, then
+    value), k_rope [Tk, rope] bf16, offsets cu_q, cu_k [B + 1] int32."""
+    Tq, H, _ = _dim(q, 3, "q")
+    dev = _same_device(q, kv, k_rope, cu_q, cu_k, out, lse)
+    if out is None:
+        out = _new((Tq, H, cfg.v_dim), out_dtype, dev, stream)
+    if lse is None:
+        lse = _new((H, Tq), torch.float32, dev, stream)
+    _check(_lib.moe_latent_attn_expanded(
+        *_expanded_args(cfg, q, kv, k_rope, cu_q, cu_k, scale, causal),
+        _dev(out, out.dtype, "out", (Tq, H, cfg.v_dim)), _dt(out), _dev(lse, torch.float32, "lse", (H, Tq)),
+        _stream(stream)), "moe_latent_attn_expanded")
+    return out, lse
+
+
+def moe_latent_attn_expanded_backward_workspace_bytes(cfg: moe_latent_config, Tq: int, Tk: int) -> int:
+    return int(_lib.moe_latent_attn_expanded_backward_workspace_bytes(ctypes.byref(cfg), Tq, Tk))
+
+
+def moe_latent_attn_expanded_backward(cfg: moe_latent_config, q: torch.Tensor, kv: torch.Tensor,
+                                      k_rope: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor, scale: float,
+                                      out: torch.Tensor, lse: torch.Tensor, dout: torch.Tensor,
+                                      causal: bool = True, dq: torch.Tensor = None, dkv: torch.Tensor = None,
+                                      dk_rope: torch.Tensor = None, grad_dtype=torch.bfloat16,
+                                      ws: torch.Tensor = None, stream=None):
+    """-> (dq, dkv, dk_rope) of the shapes of q, kv, k_rope (bf16 or f32, all alike), from
+    the forward's inputs, out (bf16) and lse and the upstream gradient dout (bf16)."""
+    Tq, H, _ = _dim(q, 3, "q")
+    Tk = _dim(kv, 3, "kv")[0]
+    dev = _same_device(q, kv, k_rope, cu_q, cu_k, out, lse, dout, dq, dkv, dk_rope, ws)
+    dq = _new(q.shape, grad_dtype, dev, stream) if dq is None else dq
+    dkv = _new(kv.shape, dq.dtype, dev, stream) if dkv is None else dkv
+    dk_rope = _new(k_rope.shape, dq.dtype, dev, stream) if dk_rope is None else dk_rope
+    if ws is None:
+        ws = _new((max(moe_latent_attn_expanded_backward_workspace_bytes(cfg, Tq, Tk), 1),), torch.uint8, dev, stream)
+    _check(_lib.moe_latent_attn_expanded_backward(
+        *_expanded_args(cfg, q, kv, k_rope, cu_q, cu_k, scale, causal),
+        _dev(out, torch.bfloat16, "out", (Tq, H, cfg.v_dim)), _dev(lse, torch.float32, "lse", (H, Tq)),
+        _dev(dout, torch.bfloat16, "dout", (Tq, H, cfg.v_dim)), _dev(dq, dq.dtype, "dq", q.shape),
+        _dev(dkv, dq.dtype, "dkv", kv.shape), _dev(dk_rope, dq.dtype, "dk_rope", k_rope.shape), _dt(dq),
+        _dev(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)), "moe_latent_attn_expanded_backward")
+    return dq, dkv, dk_rope
 
 
 from .layer import MoELayer  # noqa: E402,F401

@@ -1,0 +1,211 @@
+// Shared pieces of the latent-attention kernels: configuration checks, matrix-instruction
+// operand types, the LDS tile layout and the transposed LDS read. gfx950 only (wave64).
+//
+// All attention kernels use v_mfma_f32_32x32x16_bf16. Lane l of a wave supplies, for the
+// 32x16 operands, row (A) or column (B) l % 32 at the 8 depth positions 8 * (l / 32) + e,
+// and holds of the 32x32 result column l % 32 at rows 8 * i + 4 * (l / 32) + e (i, e < 4,
+// register 4 * i + e). A result therefore feeds the next product as its B operand without
+// leaving the lane: depth slot (l / 32, e) of step ks is given the row that register
+// 8 * ks + e holds, and the A operand is read in the same order (tr_frag).
+#pragma once
+
+#include <cmath>
+
+#include "common.h"
+
+namespace moe {
+
+typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef float f16v __attribute__((ext_vector_type(16)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) uint8_t lds_byte;
+
+constexpr int kRope = 64;
+constexpr int kMaxHeads = 1024;
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kNegInf = -__builtin_inff();
+
+// Host-side validation of a latent-attention configuration.
+inline moe_status check_latent(const moe_latent_config* c) {
+  if (!c) return MOE_ERR_NULL;
+  if (c->n_heads < 1 || c->n_heads > kMaxHeads) return MOE_ERR_SHAPE;
+  if (c->latent < 1 || c->rope < 1 || c->nope < 1 || c->v_dim < 1) return MOE_ERR_SHAPE;
+  if (c->latent != 256 && c->latent != 512) return MOE_ERR_UNSUPPORTED;
+  if (c->rope != kRope || c->nope != c->v_dim) return MOE_ERR_UNSUPPORTED;
+  if (c->nope != 64 && c->nope != 128) return MOE_ERR_UNSUPPORTED;
+  if (c->cache_kind != MOE_CACHE_BF16 && c->cache_kind != MOE_CACHE_FP8) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+inline bool good_scale(float s) { return s > 0.0f && std::isfinite(s); }
+
+inline bool misaligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+
+// An E4M3 cache row: latent codes, rope bf16 values, one float scale per 128 codes.
+constexpr int fp8_row_bytes(int latent) { return (latent + 2 * kRope + 4 * (latent / kTile) + 15) / 16 * 16; }
+constexpr int cache_row_bytes(int latent, bool fp8) { return fp8 ? fp8_row_bytes(latent) : 2 * (latent + kRope); }
+
+// ---------------------------------------------------------------------------------
+// Device helpers
+// ---------------------------------------------------------------------------------
+__device__ __forceinline__ f16v mfma(bf8 a, bf8 b, f16v c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ f16v zero16() {
+  f16v z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.0f;
+  return z;
+}
+
+// The value of the lane 32 away combined with the own one.
+__device__ __forceinline__ float half_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Registers 8 * ks .. 8 * ks + 7 of a result as the B operand of depth step ks.
+__device__ __forceinline__ bf8 b_operand(const f16v& s, int ks) {
+  union { uint32_t u[4]; bf8 v; } r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.u[i] = pack_bf16x2(s[8 * ks + 2 * i], s[8 * ks + 2 * i + 1]);
+  return r.v;
+}
+
+// Eight E4M3 codes times a power-of-two scale, as bf16 (exact: four significant bits).
+__device__ __forceinline__ u4 unpack_fp8(uint2 q, float s) {
+  typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+  const bf2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q.x, s, false);
+  const bf2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q.x, s, true);
+  const bf2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q.y, s, false);
+  const bf2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q.y, s, true);
+  return u4{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, c),
+            __builtin_bit_cast(uint32_t, d)};
+}
+
+// LDS tiles hold rows of W bytes (a power of two from 128) in 16-byte chunks. The 64 banks
+// span 256 bytes, so the chunks of each 256 bytes are permuted by the row such that both
+// kinds of read touch every bank once: 16 consecutive rows at one chunk (ds_read_b128), and
+// 4 consecutive rows at 4 adjacent chunks (two transposed reads). Measured on
+// one CU: 196 bytes a clock so permuted, 120 with an 8-chunk permutation.
+__device__ __forceinline__ constexpr int row_key(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
+// Chunk c of row r sits at chunk c ^ row_key(r) of its 256 bytes; two 128-byte rows share
+// one 256-byte line.
+template <int W>
+__device__ __forceinline__ int tile_off(int r, int c) {
+  if constexpr (W >= 256) return r * W + ((c ^ row_key(r)) << 4);
+  else return (r >> 1) * 256 + (((((r & 1) << 3) | c) ^ ((((r >> 1) & 1) << 2) | ((r >> 2) & 3))) << 4);
+}
+
+// A operand (32 rows x 16 depth) from a tile whose rows are the operand's rows r0 + l % 32
+// (r0 a multiple of 32), chunks 2 s and 2 s + 1: the lane's offset in row block 0 at s = 0,
+// and the read. The permutation makes the step an exclusive or of the offset.
+template <int W>
+__device__ __forceinline__ int row_base(int lane) { return tile_off<W>(lane & 31, lane >> 5); }
+template <int W>
+__device__ __forceinline__ bf8 row_frag(const uint8_t* t, int base, int r0, int s) {
+  return *reinterpret_cast<const bf8*>(t + (r0 * W + (s >> 3) * 256) + (base ^ ((s & 7) << 5)));
+}
+
+// A operand (32 columns x 16 rows) of a tile read transposed: operand row m is column
+// 32 d + m, depth slot (h, e) is tile row r0 + 8 * (e / 4) + 4 * h + e % 4 (r0 a multiple
+// of 16). ds_read_b64_tr_b16: of 16 lanes, lane u gives the address of 4 columns of row
+// u / 4 and gets column u of the 4 rows.
+template <int W>
+__device__ __forceinline__ int tr_base(int lane) {
+  const int half = (lane >> 4) & 1, h = lane >> 5, u = lane & 15;
+  return tile_off<W>(4 * h + (u >> 2), 2 * half + ((u & 3) >> 1)) + ((u & 1) << 3);
+}
+template <int W>
+__device__ __forceinline__ bf8 tr_frag(const uint8_t* t, int base, int r0, int d) {
+  typedef __attribute__((address_space(3))) bf4 lds_bf4;
+  const uint8_t* p = t + (d >> 2) * 256;
+  const bf4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf4*)(p + r0 * W + (base ^ ((d & 3) << 6))));
+  const bf4 hi =
+      __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf4*)(p + (r0 + 8) * W + (base ^ (((d & 3) << 6) | 32))));
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+template <typename T>
+__device__ __forceinline__ T* wave_uniform(T* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return reinterpret_cast<T*>(((uint64_t)hi << 32) | lo);
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(wave_uniform(const_cast<void*>(base)), 0,
+                                           __builtin_amdgcn_readfirstlane((int)(uint32_t)bytes), 0x00020000);
+}
+
+// Copies ROWS rows of W bytes (W = 128 or 256) from a buffer into an LDS tile, without
+// passing registers: NW waves, each instruction 1024 bytes. Rows past the buffer's end
+// read as zero.
+template <int W, int ROWS, int NW>
+__device__ __forceinline__ void tile_copy(__amdgpu_buffer_rsrc_t src, int stride, int col, uint8_t* t,
+                                          int wave, int lane) {
+  constexpr int kInstr = ROWS * W / 1024;
+  static_assert(kInstr % NW == 0, "copies per wave");
+  const int pos = lane & 15;
+#pragma unroll
+  for (int j = 0; j < kInstr / NW; ++j) {
+    const int i = j * NW + wave;       // 256-byte lines 4 i .. 4 i + 3
+    const int line = 4 * i + (lane >> 4);
+    int r, c;
+    if constexpr (W == 256) {
+      r = line;
+      c = pos ^ row_key(line);
+    } else {
+      const int x = pos ^ (((line & 1) << 2) | ((line >> 1) & 3));
+      r = 2 * line + (x >> 3);
+      c = x & 7;
+    }
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (lds_byte*)(t + i * 1024), 16, r * stride + col + c * 16,
+                                             0, 0, 0);
+  }
+}
+
+// Every wave of the workgroup waits for its own vector-memory and LDS operations, then for
+// the others.
+__device__ __forceinline__ void copies_done_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0), no export wait
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// The sequence that holds tile slot `slot` when sequence b owns the slots from
+// off[b] / TILE + b on (its tiles first; a slot after them is empty). The starts do not
+// decrease, so the sequence is the last whose start is at most `slot`.
+struct SeqTile {
+  int b, tile;
+};
+template <int TILE>
+__device__ __forceinline__ SeqTile find_seq(const int32_t* off, int B, int64_t slot) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((int64_t)(max(off[mid], 0) / TILE) + mid <= slot) lo = mid; else hi = mid - 1;
+  }
+  return {lo, (int)min((int64_t)0x3fffffff, slot - ((int64_t)(max(off[lo], 0) / TILE) + lo))};
+}
+
+// A value kept as bf16 or float by a flag.
+__device__ __forceinline__ void store4(void* base, int64_t at, bool bf16, float a, float b, float c, float d) {
+  if (bf16) {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + at) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
+  } else {
+    *reinterpret_cast<float4*>(static_cast<float*>(base) + at) = make_float4(a, b, c, d);
+  }
+}
+
+}  // namespace moe

@@ -1,0 +1,363 @@
+// Gradients of the attention over expanded keys and values.
+//
+// With P = exp(s - lse) recomputed tile by tile and D = rowsum(dO * O):
+//   dV = P^T dO,  dS = P * (dO V^T - D),  dK = scale dS^T Q,  dQ = scale dS K.
+// Two kernels, one per side of the score matrix, so that every sum stays in the registers
+// of one wave in a fixed order (no atomics): the first owns 32 keys a wave and walks the
+// queries (dK, dV), the second owns 32 queries a wave and walks the keys (dQ). Scores are
+// formed twice; the alternative, keeping dS, would move H * Tq * Tk values through memory.
+// The rotary key is shared by the heads: each head's part of its gradient goes to a
+// workspace and a last kernel sums the heads in order. P and dS are rounded to bf16 for
+// the matrix instructions, as the inputs are; everything else is FP32.
+#include "latent.h"
+
+namespace moe {
+namespace {
+
+constexpr int kBWaves = 4;
+constexpr int kBRows = 32 * kBWaves;   // keys (or queries) a workgroup owns
+constexpr int kBTile = 64;             // queries (or keys) a step
+
+struct BackwardArgs {
+  const uint16_t *q, *kv, *kr, *dout;
+  const int32_t *cu_q, *cu_k;
+  const float *lse, *delta;   // [H, Tq]
+  void *dq, *dkv;
+  float* dkr_part;            // [H, Tk, rope]
+  int64_t Tq, Tk;
+  int B, H;
+  float scale, scale2;        // scale2 = scale * log2(e)
+  int causal, bf16;
+};
+
+struct Span {
+  int64_t q0, k0;   // first query and key of the sequence
+  int nq, nk;
+};
+__device__ __forceinline__ Span span_of(const BackwardArgs& a, int b) {
+  Span s;
+  s.q0 = min((int64_t)max(a.cu_q[b], 0), a.Tq);
+  s.k0 = min((int64_t)max(a.cu_k[b], 0), a.Tk);
+  s.nq = max((int)(min((int64_t)a.cu_q[b + 1], a.Tq) - s.q0), 0);
+  s.nk = max((int)(min((int64_t)a.cu_k[b + 1], a.Tk) - s.k0), 0);
+  return s;
+}
+
+// delta[h][t] = sum over the value width of dout * out; 16 lanes a (token, head) row.
+template <int D>
+__global__ __launch_bounds__(256) void delta_kernel(const uint16_t* __restrict__ out,
+                                                    const uint16_t* __restrict__ dout, int64_t T, int H,
+                                                    float* __restrict__ delta) {
+  const int64_t r = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 16;
+  const int sub = threadIdx.x & 15;
+  float sum = 0.0f;
+  if (r < T * H) {
+    constexpr int kPer = D / 16;
+    const uint16_t *a = out + r * D + sub * kPer, *b = dout + r * D + sub * kPer;
+#pragma unroll
+    for (int i = 0; i < kPer; i += 4) {
+      const uint2 x = *reinterpret_cast<const uint2*>(a + i), y = *reinterpret_cast<const uint2*>(b + i);
+      sum = fmaf(__uint_as_float(x.x << 16), __uint_as_float(y.x << 16), sum);
+      sum = fmaf(__uint_as_float(x.x & 0xffff0000u), __uint_as_float(y.x & 0xffff0000u), sum);
+      sum = fmaf(__uint_as_float(x.y << 16), __uint_as_float(y.y << 16), sum);
+      sum = fmaf(__uint_as_float(x.y & 0xffff0000u), __uint_as_float(y.y & 0xffff0000u), sum);
+    }
+  }
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 16);
+  if (r < T * H && sub == 0) delta[(r % H) * T + r / H] = sum;
+}
+
+// ---------------------------------------------------------------------------------
+// dK, dV
+// ---------------------------------------------------------------------------------
+template <int D>
+struct __attribute__((aligned(256))) QTile {
+  uint8_t q[kBTile * 2 * D], r[kBTile * 2 * kRope], g[kBTile * 2 * D];   // q (nope, rope), dout
+  float lse[kBTile], delta[kBTile];
+};
+
+template <int D>
+__device__ __forceinline__ void copy_q(const BackwardArgs& a, QTile<D>* t, int64_t row0, int n, int h, int wave,
+                                       int lane) {
+  const int qs = a.H * 2 * (D + kRope), gs = a.H * 2 * D;
+  const auto q = buffer_of(a.q + (row0 * a.H + h) * (D + kRope), (int64_t)n * qs);
+  const auto g = buffer_of(a.dout + (row0 * a.H + h) * D, (int64_t)n * gs);
+  tile_copy<2 * D, kBTile, kBWaves>(q, qs, 0, t->q, wave, lane);
+  tile_copy<2 * kRope, kBTile, kBWaves>(q, qs, 2 * D, t->r, wave, lane);
+  tile_copy<2 * D, kBTile, kBWaves>(g, gs, 0, t->g, wave, lane);
+  if (wave < 2) {   // a value a lane
+    const float* src = wave == 0 ? a.lse : a.delta;
+    const auto s = buffer_of(src + (int64_t)h * a.Tq + row0, (int64_t)n * 4);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(s, (lds_byte*)(wave == 0 ? t->lse : t->delta), 4, lane * 4, 0, 0, 0);
+  }
+}
+
+template <int D>
+__global__ __launch_bounds__(kBWaves* kWave, 1) void backward_kv_kernel(const BackwardArgs a) {
+  constexpr int kSteps = (D + kRope) / 16;
+  __shared__ QTile<D> tiles[2];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 31, hh = lane >> 5;
+  const int h = blockIdx.x % a.H;
+  const SeqTile st = find_seq<kBRows>(a.cu_k, a.B, blockIdx.x / a.H);
+  const Span sp = span_of(a, st.b);
+  if (st.tile < 0 || (int64_t)st.tile * kBRows >= sp.nk) return;
+  const int w0 = st.tile * kBRows + wave * 32;   // the wave's first key
+  const int key = w0 + col;
+  const int ahead = sp.nk - sp.nq;                // query i sees keys j <= i + ahead when causal
+
+  bf8 kf[kSteps], vf[D / 16];
+  {
+    const int64_t kc = sp.k0 + min(key, sp.nk - 1);
+    const uint16_t* kp = a.kv + (kc * a.H + h) * 2 * D + 8 * hh;
+    const uint16_t* rp = a.kr + kc * kRope + 8 * hh;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      kf[s] = *reinterpret_cast<const bf8*>(kp + 16 * s);
+      vf[s] = *reinterpret_cast<const bf8*>(kp + D + 16 * s);
+    }
+#pragma unroll
+    for (int s = 0; s < kRope / 16; ++s) kf[D / 16 + s] = *reinterpret_cast<const bf8*>(rp + 16 * s);
+  }
+  f16v dk[D / 32], dr[kRope / 32], dv[D / 32];
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d) dk[d] = dv[d] = zero16();
+#pragma unroll
+  for (int d = 0; d < kRope / 32; ++d) dr[d] = zero16();
+  const int qb = row_base<2 * D>(lane), rb = row_base<2 * kRope>(lane);
+  const int qt = tr_base<2 * D>(lane), rt = tr_base<2 * kRope>(lane);
+
+  // queries from the first that sees this workgroup's first key
+  const int first = a.causal ? max(0, st.tile * kBRows - ahead) / kBTile * kBTile : 0;
+  if (first < sp.nq) copy_q<D>(a, &tiles[0], sp.q0 + first, min(kBTile, sp.nq - first), h, wave, lane);
+  for (int t0 = first, it = 0; t0 < sp.nq; t0 += kBTile, ++it) {
+    copies_done_barrier();
+    if (t0 + kBTile < sp.nq)
+      copy_q<D>(a, &tiles[(it + 1) & 1], sp.q0 + t0 + kBTile, min(kBTile, sp.nq - t0 - kBTile), h, wave, lane);
+    const QTile<D>& tl = tiles[it & 1];
+    const bool edge = a.causal && t0 + ahead < w0 + 31;   // some query hides some key
+#pragma unroll
+    for (int f = 0; f < kBTile / 32; ++f) {
+      f16v s = zero16(), dp = zero16();
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) s = mfma(row_frag<2 * D>(tl.q, qb, 32 * f, i), kf[i], s);
+#pragma unroll
+      for (int i = 0; i < kRope / 16; ++i) s = mfma(row_frag<2 * kRope>(tl.r, rb, 32 * f, i), kf[D / 16 + i], s);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) dp = mfma(row_frag<2 * D>(tl.g, qb, 32 * f, i), vf[i], dp);
+      // queries past the end were read as zeros: lse 0, score 0, dout 0, so they add nothing
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f4 ls = *reinterpret_cast<const f4*>(tl.lse + 32 * f + 8 * i + 4 * hh);
+        const f4 de = *reinterpret_cast<const f4*>(tl.delta + 32 * f + 8 * i + 4 * hh);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 4 * i + e;
+          float p = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale2, -ls[e] * kLog2e));
+          if (edge && key > t0 + 32 * f + 8 * i + 4 * hh + e + ahead) p = 0.0f;
+          s[r] = p;
+          dp[r] = p * (dp[r] - de[e]);
+        }
+      }
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const bf8 p = b_operand(s, ks), ds = b_operand(dp, ks);
+        const int r0 = 32 * f + 16 * ks;
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) {
+          dv[d] = mfma(tr_frag<2 * D>(tl.g, qt, r0, d), p, dv[d]);
+          dk[d] = mfma(tr_frag<2 * D>(tl.q, qt, r0, d), ds, dk[d]);
+        }
+#pragma unroll
+        for (int d = 0; d < kRope / 32; ++d) dr[d] = mfma(tr_frag<2 * kRope>(tl.r, rt, r0, d), ds, dr[d]);
+      }
+    }
+  }
+  if (key >= sp.nk) return;
+  const int64_t at = ((sp.k0 + key) * a.H + h) * 2 * D + 4 * hh;
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      store4(a.dkv, at + 32 * d + 8 * i, a.bf16, dk[d][4 * i] * a.scale, dk[d][4 * i + 1] * a.scale,
+             dk[d][4 * i + 2] * a.scale, dk[d][4 * i + 3] * a.scale);
+      store4(a.dkv, at + D + 32 * d + 8 * i, a.bf16, dv[d][4 * i], dv[d][4 * i + 1], dv[d][4 * i + 2],
+             dv[d][4 * i + 3]);
+    }
+  float* rp = a.dkr_part + ((int64_t)h * a.Tk + sp.k0 + key) * kRope + 4 * hh;
+#pragma unroll
+  for (int d = 0; d < kRope / 32; ++d)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      store4(rp, 32 * d + 8 * i, false, dr[d][4 * i], dr[d][4 * i + 1], dr[d][4 * i + 2], dr[d][4 * i + 3]);
+}
+
+// dk_rope[t] = scale * sum of the heads' parts in head order, for tokens of a sequence.
+__global__ __launch_bounds__(256) void rope_sum_kernel(const float* __restrict__ part,
+                                                       const int32_t* __restrict__ cu_k, int B, int64_t Tk,
+                                                       int H, float scale, void* __restrict__ out, int bf16) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, t = i / kRope;
+  if (t >= Tk || t < cu_k[0] || t >= cu_k[B]) return;
+  f4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int h = 0; h < H; ++h) sum += *reinterpret_cast<const f4*>(part + (int64_t)h * Tk * kRope + i);
+  store4(out, i, bf16, sum[0] * scale, sum[1] * scale, sum[2] * scale, sum[3] * scale);
+}
+
+// ---------------------------------------------------------------------------------
+// dQ
+// ---------------------------------------------------------------------------------
+template <int D>
+struct __attribute__((aligned(256))) KTile {
+  uint8_t k[kBTile * 2 * D], r[kBTile * 2 * kRope], v[kBTile * 2 * D];
+};
+
+template <int D>
+__device__ __forceinline__ void copy_k(const BackwardArgs& a, KTile<D>* t, int64_t key0, int n, int h, int wave,
+                                       int lane) {
+  const int stride = a.H * 4 * D;
+  const auto kv = buffer_of(a.kv + (key0 * a.H + h) * 2 * D, (int64_t)n * stride);
+  const auto kr = buffer_of(a.kr + key0 * kRope, (int64_t)n * 2 * kRope);
+  tile_copy<2 * D, kBTile, kBWaves>(kv, stride, 0, t->k, wave, lane);
+  tile_copy<2 * kRope, kBTile, kBWaves>(kr, 2 * kRope, 0, t->r, wave, lane);
+  tile_copy<2 * D, kBTile, kBWaves>(kv, stride, 2 * D, t->v, wave, lane);
+}
+
+template <int D>
+__global__ __launch_bounds__(kBWaves* kWave, 1) void backward_q_kernel(const BackwardArgs a) {
+  constexpr int kSteps = (D + kRope) / 16;
+  __shared__ KTile<D> tiles[2];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 31, hh = lane >> 5;
+  const int h = blockIdx.x % a.H;
+  const SeqTile st = find_seq<kBRows>(a.cu_q, a.B, blockIdx.x / a.H);
+  const Span sp = span_of(a, st.b);
+  if (st.tile < 0 || (int64_t)st.tile * kBRows >= sp.nq) return;
+  const int wg0 = st.tile * kBRows, w0 = wg0 + wave * 32, row = w0 + col;
+  const int ahead = sp.nk - sp.nq;
+  const int limit = a.causal ? min(sp.nk, row + ahead + 1) : sp.nk;
+  const int wg_limit = a.causal ? min(sp.nk, min(wg0 + kBRows, sp.nq) + ahead) : sp.nk;
+  const int n_tiles = max(0, (wg_limit + kBTile - 1) / kBTile);
+
+  bf8 qf[kSteps], gf[D / 16];
+  const int64_t rc = sp.q0 + min(row, sp.nq - 1);
+  {
+    const uint16_t* qp = a.q + (rc * a.H + h) * (D + kRope) + 8 * hh;
+    const uint16_t* gp = a.dout + (rc * a.H + h) * D + 8 * hh;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) qf[s] = *reinterpret_cast<const bf8*>(qp + 16 * s);
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) gf[s] = *reinterpret_cast<const bf8*>(gp + 16 * s);
+  }
+  const float lse2 = a.lse[(int64_t)h * a.Tq + rc] * kLog2e, delta = a.delta[(int64_t)h * a.Tq + rc];
+  f16v dq[D / 32 + kRope / 32];
+#pragma unroll
+  for (int d = 0; d < D / 32 + kRope / 32; ++d) dq[d] = zero16();
+  const int kb = row_base<2 * D>(lane), rb = row_base<2 * kRope>(lane);
+  const int kt = tr_base<2 * D>(lane), rt = tr_base<2 * kRope>(lane);
+
+  if (n_tiles > 0) copy_k<D>(a, &tiles[0], sp.k0, min(kBTile, sp.nk), h, wave, lane);
+  for (int t = 0; t < n_tiles; ++t) {
+    copies_done_barrier();
+    const int k0 = t * kBTile;
+    if (t + 1 < n_tiles)
+      copy_k<D>(a, &tiles[(t + 1) & 1], sp.k0 + k0 + kBTile, min(kBTile, sp.nk - k0 - kBTile), h, wave, lane);
+    const KTile<D>& tl = tiles[t & 1];
+    const bool edge = k0 + kBTile > (a.causal ? min(sp.nk, w0 + ahead + 1) : sp.nk);
+#pragma unroll
+    for (int f = 0; f < kBTile / 32; ++f) {
+      f16v s = zero16(), dp = zero16();
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) s = mfma(row_frag<2 * D>(tl.k, kb, 32 * f, i), qf[i], s);
+#pragma unroll
+      for (int i = 0; i < kRope / 16; ++i) s = mfma(row_frag<2 * kRope>(tl.r, rb, 32 * f, i), qf[D / 16 + i], s);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) dp = mfma(row_frag<2 * D>(tl.v, kb, 32 * f, i), gf[i], dp);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        float p = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale2, -lse2));
+        if (edge && k0 + 32 * f + 8 * (r / 4) + 4 * hh + r % 4 >= limit) p = 0.0f;
+        dp[r] = p * (dp[r] - delta);
+      }
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const bf8 ds = b_operand(dp, ks);
+        const int r0 = 32 * f + 16 * ks;
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) dq[d] = mfma(tr_frag<2 * D>(tl.k, kt, r0, d), ds, dq[d]);
+#pragma unroll
+        for (int d = 0; d < kRope / 32; ++d)
+          dq[D / 32 + d] = mfma(tr_frag<2 * kRope>(tl.r, rt, r0, d), ds, dq[D / 32 + d]);
+      }
+    }
+  }
+  if (row >= sp.nq) return;
+  const int64_t at = ((sp.q0 + row) * a.H + h) * (D + kRope) + 4 * hh;
+#pragma unroll
+  for (int d = 0; d < D / 32 + kRope / 32; ++d)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      store4(a.dq, at + 32 * d + 8 * i, a.bf16, dq[d][4 * i] * a.scale, dq[d][4 * i + 1] * a.scale,
+             dq[d][4 * i + 2] * a.scale, dq[d][4 * i + 3] * a.scale);
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+template <int D>
+void launch_backward(BackwardArgs& a, const uint16_t* out, float* delta, void* dk_rope, hipStream_t s) {
+  const int64_t rows = a.Tq * a.H;
+  if (a.Tq > 0) {
+    hipLaunchKernelGGL(delta_kernel<D>, dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, s, out, a.dout, a.Tq, a.H,
+                       delta);
+    hipLaunchKernelGGL(backward_q_kernel<D>, dim3((unsigned)((a.Tq / kBRows + a.B) * a.H)),
+                       dim3(kBWaves * kWave), 0, s, a);
+  }
+  if (a.Tk > 0) {
+    hipLaunchKernelGGL(backward_kv_kernel<D>, dim3((unsigned)((a.Tk / kBRows + a.B) * a.H)),
+                       dim3(kBWaves * kWave), 0, s, a);
+    hipLaunchKernelGGL(rope_sum_kernel, dim3((unsigned)((a.Tk * kRope / 4 + 255) / 256)), dim3(256), 0, s,
+                       a.dkr_part, a.cu_k, a.B, a.Tk, a.H, a.scale, dk_rope, a.bf16);
+  }
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t moe_latent_attn_expanded_backward_workspace_bytes(const moe_latent_config* cfg, int64_t Tq,
+                                                                    int64_t Tk) {
+  if (check_latent(cfg) != MOE_OK || Tq < 0 || Tk < 0 || Tq > 0x7fffffff || Tk > 0x7fffffff) return 0;
+  return align256((size_t)Tq * cfg->n_heads * 4) + (size_t)Tk * cfg->n_heads * kRope * 4;
+}
+
+extern "C" moe_status moe_latent_attn_expanded_backward(
+    const moe_latent_config* cfg, int64_t B, int64_t Tq, int64_t Tk, const uint16_t* q, const uint16_t* kv,
+    const uint16_t* k_rope, const int32_t* cu_q, const int32_t* cu_k, float scale, int32_t causal,
+    const uint16_t* out, const float* lse, const uint16_t* dout, void* dq, void* dkv, void* dk_rope, moe_dtype gt,
+    void* ws, size_t ws_bytes, void* stream) {
+  const moe_status st = check_latent(cfg);
+  if (st != MOE_OK) return st;
+  if (B < 0 || B > 0x3fffffff || Tq < 0 || Tq > 0x7fffffff || Tk < 0 || Tk > 0x7fffffff) return MOE_ERR_SHAPE;
+  if (!good_scale(scale)) return MOE_ERR_SHAPE;
+  if (gt != MOE_BF16 && gt != MOE_F32) return MOE_ERR_DTYPE;
+  if (B == 0 || (Tq == 0 && Tk == 0)) return MOE_OK;
+  if (!cu_q || !cu_k) return MOE_ERR_NULL;
+  if (Tq > 0 && (!q || !out || !lse || !dout || !dq)) return MOE_ERR_NULL;
+  if (Tk > 0 && (!kv || !k_rope || !dkv || !dk_rope)) return MOE_ERR_NULL;
+  const void* vecs[] = {q, kv, k_rope, out, dout, dq, dkv, dk_rope, ws};
+  for (const void* p : vecs)
+    if (misaligned16(p)) return MOE_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < moe_latent_attn_expanded_backward_workspace_bytes(cfg, Tq, Tk)) return MOE_ERR_WORKSPACE;
+  if ((Tq / kBRows + B) * cfg->n_heads > 0x7fffffff || (Tk / kBRows + B) * cfg->n_heads > 0x7fffffff)
+    return MOE_ERR_UNSUPPORTED;
+  if (Tq * cfg->n_heads > (int64_t)1 << 34) return MOE_ERR_UNSUPPORTED;
+  float* delta = static_cast<float*>(ws);
+  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256((size_t)Tq * cfg->n_heads * 4));
+  BackwardArgs a{q, kv, k_rope, dout, cu_q, cu_k, lse, delta, dq, dkv, part, Tq, Tk, (int)B, cfg->n_heads,
+                 scale, scale * kLog2e, causal != 0, gt == MOE_BF16};
+  if (cfg->nope == 128) launch_backward<128>(a, out, delta, dk_rope, as_stream(stream));
+  else launch_backward<64>(a, out, delta, dk_rope, as_stream(stream));
+  return launch_status();
+}

@@ -1,0 +1,193 @@
+// The paged latent cache: rows [c | rotary key] written as bf16 or as E4M3 codes with a
+// power-of-two scale per 128 values, and read back as bf16. HBM-bound: one read and one
+// write of each row.
+#include "latent.h"
+
+namespace moe {
+namespace {
+
+// 16 lanes a 128-value tile (and 16, half of them idle, for the rotary key), 8 values a
+// lane. part = tile index, or R / 128 for the rotary key.
+template <int R, typename T, bool FP8>
+__global__ __launch_bounds__(256) void cache_write_kernel(const T* __restrict__ x, int64_t ldx, int64_t n,
+                                                          const int32_t* __restrict__ slots,
+                                                          uint8_t* __restrict__ cache, int64_t n_slots) {
+  constexpr int kParts = R / kTile + 1;
+  const int64_t g = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 4;
+  const int sub = threadIdx.x & 15;
+  const int64_t t = g / kParts;
+  const int part = (int)(g % kParts);
+  if (t >= n) return;
+  const int64_t slot = slots[t];
+  if (slot < 0 || slot >= n_slots) return;
+  const bool rope = part == kParts - 1;
+  if (rope && sub >= kRope / 8) return;
+  const T* src = x + t * ldx + part * kTile + sub * 8;
+  uint8_t* row = cache + slot * cache_row_bytes(R, FP8);
+  float v[8];
+  u4 raw;
+  if constexpr (sizeof(T) == 2) {
+    raw = *reinterpret_cast<const u4*>(src);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(raw[i] << 16);
+      v[2 * i + 1] = __uint_as_float(raw[i] & 0xffff0000u);
+    }
+  } else {
+    const float4 a = *reinterpret_cast<const float4*>(src), b = *reinterpret_cast<const float4*>(src + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) raw[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+  }
+  if (!FP8 || rope) {
+    const int at = FP8 ? R + sub * 16 : (part * kTile + sub * 8) * 2;
+    *reinterpret_cast<u4*>(row + at) = raw;
+    return;
+  }
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
+  amax = group_max<16>(amax);
+  const float s = group_scale_pow2(amax), inv = inv_pow2(s);
+  *reinterpret_cast<uint2*>(row + part * kTile + sub * 8) =
+      make_uint2(e4m3_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                 e4m3_pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+  if (sub == 0) *reinterpret_cast<float*>(row + R + 2 * kRope + 4 * part) = s;
+}
+
+// A workgroup reads kReadRows output rows: their cache rows are looked up once, then all
+// threads copy 16-byte output pieces.
+constexpr int kReadRows = 16;
+
+template <int R, bool FP8>
+__global__ __launch_bounds__(256) void cache_read_kernel(const uint8_t* __restrict__ cache, int64_t n_pages,
+                                                         int32_t page, const int32_t* __restrict__ table,
+                                                         int B, int64_t max_pages,
+                                                         const int32_t* __restrict__ cu,
+                                                         const int32_t* __restrict__ starts, int64_t n,
+                                                         uint16_t* __restrict__ out) {
+  __shared__ int64_t row_of[kReadRows];
+  const int64_t r0 = (int64_t)blockIdx.x * kReadRows;
+  if (threadIdx.x < kReadRows) {
+    const int64_t r = r0 + threadIdx.x;
+    int64_t at = -1;
+    if (B > 0 && r < n && r >= cu[0] && r < cu[B]) {
+      int lo = 0, hi = B - 1;   // the last sequence that starts at or before r
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu[mid] <= r) lo = mid; else hi = mid - 1;
+      }
+      const int64_t p = r - cu[lo] + (starts ? starts[lo] : 0);
+      if (p >= 0 && p / page < max_pages) {
+        const int64_t pg = table[lo * max_pages + p / page];
+        if (pg >= 0 && pg < n_pages) at = pg * page + p % page;
+      }
+    }
+    row_of[threadIdx.x] = at;
+  }
+  __syncthreads();
+  constexpr int kPieces = (R + kRope) / 8;
+  for (int i = threadIdx.x; i < kReadRows * kPieces; i += 256) {
+    const int rr = i / kPieces, p = i % kPieces;
+    if (r0 + rr >= n) break;
+    u4 v = {0, 0, 0, 0};
+    if (row_of[rr] >= 0) {
+      const uint8_t* row = cache + row_of[rr] * cache_row_bytes(R, FP8);
+      if constexpr (FP8) {
+        if (p < R / 8) {
+          const uint2 q = *reinterpret_cast<const uint2*>(row + p * 8);
+          const float s = *reinterpret_cast<const float*>(row + R + 2 * kRope + 4 * (p / 16));
+          v = unpack_fp8(q, s);
+        } else {
+          v = *reinterpret_cast<const u4*>(row + R + (p - R / 8) * 16);
+        }
+      } else {
+        v = *reinterpret_cast<const u4*>(row + p * 16);
+      }
+    }
+    *reinterpret_cast<u4*>(out + (r0 + rr) * (R + kRope) + p * 8) = v;
+  }
+}
+
+template <int R, typename T>
+void launch_write(bool fp8, const void* x, int64_t ldx, int64_t n, const int32_t* slots, void* cache,
+                  int64_t n_slots, hipStream_t s) {
+  const int64_t lanes = n * (R / kTile + 1) * 16;
+  const dim3 grid((unsigned)((lanes + 255) / 256));
+  if (fp8)
+    hipLaunchKernelGGL((cache_write_kernel<R, T, true>), grid, dim3(256), 0, s, static_cast<const T*>(x), ldx,
+                       n, slots, static_cast<uint8_t*>(cache), n_slots);
+  else
+    hipLaunchKernelGGL((cache_write_kernel<R, T, false>), grid, dim3(256), 0, s, static_cast<const T*>(x), ldx,
+                       n, slots, static_cast<uint8_t*>(cache), n_slots);
+}
+
+template <int R>
+void launch_read(bool fp8, const void* cache, int64_t n_pages, int32_t page, const int32_t* table, int64_t B,
+                 int64_t max_pages, const int32_t* cu, const int32_t* starts, int64_t n, uint16_t* out,
+                 hipStream_t s) {
+  const dim3 grid((unsigned)((n + kReadRows - 1) / kReadRows));
+  const uint8_t* c = static_cast<const uint8_t*>(cache);
+  if (fp8)
+    hipLaunchKernelGGL((cache_read_kernel<R, true>), grid, dim3(256), 0, s, c, n_pages, page, table, (int)B,
+                       max_pages, cu, starts, n, out);
+  else
+    hipLaunchKernelGGL((cache_read_kernel<R, false>), grid, dim3(256), 0, s, c, n_pages, page, table, (int)B,
+                       max_pages, cu, starts, n, out);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t moe_latent_cache_row_bytes(const moe_latent_config* cfg) {
+  if (check_latent(cfg) != MOE_OK) return 0;
+  return (size_t)cache_row_bytes(cfg->latent, cfg->cache_kind == MOE_CACHE_FP8);
+}
+
+extern "C" moe_status moe_latent_cache_write(const moe_latent_config* cfg, int64_t T, const void* x,
+                                             moe_dtype xt, int64_t x_stride, const int32_t* slots, void* cache,
+                                             int64_t n_slots, void* stream) {
+  const moe_status st = check_latent(cfg);
+  if (st != MOE_OK) return st;
+  if (T < 0 || T > 0x7fffffff || n_slots < 0 || n_slots > 0x7fffffff) return MOE_ERR_SHAPE;
+  if (x_stride < cfg->latent + cfg->rope || x_stride > ((int64_t)1 << 31)) return MOE_ERR_SHAPE;
+  if (xt != MOE_F32 && xt != MOE_BF16) return MOE_ERR_DTYPE;
+  if (T == 0 || n_slots == 0) return MOE_OK;
+  if (!x || !slots || !cache) return MOE_ERR_NULL;
+  if (misaligned16(x) || misaligned16(cache) || x_stride % (xt == MOE_BF16 ? 8 : 4)) return MOE_ERR_UNSUPPORTED;
+  const bool fp8 = cfg->cache_kind == MOE_CACHE_FP8;
+  hipStream_t s = as_stream(stream);
+  if (cfg->latent == 512) {
+    if (xt == MOE_BF16) launch_write<512, uint16_t>(fp8, x, x_stride, T, slots, cache, n_slots, s);
+    else launch_write<512, float>(fp8, x, x_stride, T, slots, cache, n_slots, s);
+  } else {
+    if (xt == MOE_BF16) launch_write<256, uint16_t>(fp8, x, x_stride, T, slots, cache, n_slots, s);
+    else launch_write<256, float>(fp8, x, x_stride, T, slots, cache, n_slots, s);
+  }
+  return launch_status();
+}
+
+extern "C" moe_status moe_latent_cache_read(const moe_latent_config* cfg, const void* cache, int64_t n_pages,
+                                            int32_t page_size, const int32_t* page_table, int64_t B,
+                                            int64_t max_pages, const int32_t* cu_rows, const int32_t* starts,
+                                            int64_t n_out, uint16_t* out, void* stream) {
+  const moe_status st = check_latent(cfg);
+  if (st != MOE_OK) return st;
+  if (n_pages < 0 || page_size < 1 || n_pages > 0x7fffffff || n_pages * page_size > 0x7fffffff) return MOE_ERR_SHAPE;
+  if (B < 0 || B > 0x7ffffffe || max_pages < 0 || max_pages > 0x7fffffff) return MOE_ERR_SHAPE;
+  if (n_out < 0 || n_out > 0x7fffffff) return MOE_ERR_SHAPE;
+  if (n_out == 0) return MOE_OK;
+  if (!out || (B > 0 && (!cu_rows || (max_pages > 0 && !page_table))) || (n_pages > 0 && !cache)) return MOE_ERR_NULL;
+  if (misaligned16(out) || misaligned16(cache)) return MOE_ERR_UNSUPPORTED;
+  const bool fp8 = cfg->cache_kind == MOE_CACHE_FP8;
+  if (cfg->latent == 512)
+    launch_read<512>(fp8, cache, n_pages, page_size, page_table, B, max_pages, cu_rows, starts, n_out, out,
+                     as_stream(stream));
+  else
+    launch_read<256>(fp8, cache, n_pages, page_size, page_table, B, max_pages, cu_rows, starts, n_out, out,
+                     as_stream(stream));
+  return launch_status();
+}

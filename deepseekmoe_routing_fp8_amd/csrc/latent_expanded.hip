@@ -1,0 +1,175 @@
+// Attention over expanded keys and values (prefill, training): forward.
+//
+// A wave owns 32 query rows. It forms S^T = K Q^T for a tile of kKeys keys (32 keys a
+// matrix result, the queries being its columns), keeps the running maximum and sum of each
+// query in the lane that holds its column, and feeds P^T, rounded to bf16, straight from
+// the result registers into O^T += V^T P^T with V read transposed from LDS. Scores,
+// maxima, sums and O stay in FP32; P's bf16 rounding (relative 2^-8 a term) is that of the
+// inputs. Keys and values reach LDS by direct copies, one tile ahead.
+#include "latent.h"
+
+namespace moe {
+namespace {
+
+constexpr int kKeys = 64;    // keys a tile
+constexpr int kFWaves = 4;   // waves of a workgroup
+constexpr int kFRows = 32 * kFWaves;
+
+struct ExpandedArgs {
+  const uint16_t *q, *kv, *kr;
+  const int32_t *cu_q, *cu_k;
+  void* out;
+  float* lse;
+  int64_t Tq, Tk;
+  int B, H;
+  float scale2;   // scale * log2(e)
+  int causal, out_bf16;
+};
+
+template <int D>
+struct __attribute__((aligned(256))) KvTile {
+  uint8_t k[kKeys * 2 * D], r[kKeys * 2 * kRope], v[kKeys * 2 * D];
+};
+
+template <int D>
+__device__ __forceinline__ void copy_kv(const ExpandedArgs& a, KvTile<D>* t, int64_t key0, int n, int h, int wave,
+                                        int lane) {
+  const int stride = a.H * 4 * D;
+  const auto kv = buffer_of(a.kv + (key0 * a.H + h) * 2 * D, (int64_t)n * stride);
+  const auto kr = buffer_of(a.kr + key0 * kRope, (int64_t)n * 2 * kRope);
+  tile_copy<2 * D, kKeys, kFWaves>(kv, stride, 0, t->k, wave, lane);
+  tile_copy<2 * kRope, kKeys, kFWaves>(kr, 2 * kRope, 0, t->r, wave, lane);
+  tile_copy<2 * D, kKeys, kFWaves>(kv, stride, 2 * D, t->v, wave, lane);
+}
+
+template <int D>
+__global__ __launch_bounds__(kFWaves* kWave, 2) void expanded_kernel(const ExpandedArgs a) {
+  constexpr int kSteps = (D + kRope) / 16;
+  __shared__ KvTile<D> tiles[2];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 31, hh = lane >> 5;
+  const int h = blockIdx.x % a.H;
+  const SeqTile st = find_seq<kFRows>(a.cu_q, a.B, blockIdx.x / a.H);
+  const int64_t tq0 = min((int64_t)max(a.cu_q[st.b], 0), a.Tq);
+  const int64_t tk0 = min((int64_t)max(a.cu_k[st.b], 0), a.Tk);
+  const int nq = (int)(min((int64_t)a.cu_q[st.b + 1], a.Tq) - tq0);
+  const int nk = max((int)(min((int64_t)a.cu_k[st.b + 1], a.Tk) - tk0), 0);
+  const int64_t q0 = (int64_t)st.tile * kFRows;
+  if (st.tile < 0 || q0 >= nq) return;
+  const int w0 = (int)q0 + wave * 32;          // the wave's first query
+  const int row = w0 + col;                    // this lane's query
+  const bool live = row < nq;
+  // keys that this lane's query sees: j < limit
+  const int limit = a.causal ? row + nk - nq + 1 : nk;
+  const int wg_limit = a.causal ? min(nk, (int)min(q0 + kFRows, (int64_t)nq) + nk - nq) : nk;
+  const int n_tiles = max(0, (wg_limit + kKeys - 1) / kKeys);
+
+  bf8 qf[kSteps];
+  {
+    const uint16_t* qp = a.q + ((tq0 + min(row, nq - 1)) * a.H + h) * (D + kRope) + 8 * hh;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) qf[s] = *reinterpret_cast<const bf8*>(qp + 16 * s);
+  }
+  f16v o[D / 32];
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d) o[d] = zero16();
+  float m = kNegInf, l = 0.0f;
+  const int kb = row_base<2 * D>(lane), rb = row_base<2 * kRope>(lane), vb = tr_base<2 * D>(lane);
+
+  if (n_tiles > 0) copy_kv<D>(a, &tiles[0], tk0, min(kKeys, nk), h, wave, lane);
+  for (int t = 0; t < n_tiles; ++t) {
+    copies_done_barrier();
+    const int k0 = t * kKeys;
+    if (t + 1 < n_tiles)
+      copy_kv<D>(a, &tiles[(t + 1) & 1], tk0 + k0 + kKeys, min(kKeys, nk - k0 - kKeys), h, wave, lane);
+    const KvTile<D>& tl = tiles[t & 1];
+    f16v s[kKeys / 32];
+#pragma unroll
+    for (int f = 0; f < kKeys / 32; ++f) {
+      s[f] = zero16();
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) s[f] = mfma(row_frag<2 * D>(tl.k, kb, 32 * f, i), qf[i], s[f]);
+#pragma unroll
+      for (int i = 0; i < kRope / 16; ++i)
+        s[f] = mfma(row_frag<2 * kRope>(tl.r, rb, 32 * f, i), qf[D / 16 + i], s[f]);
+    }
+    // scores in units of log2, hidden ones at -inf
+    const bool edge = k0 + kKeys > (a.causal ? min(nk, w0 + nk - nq + 1) : nk);
+    float top = kNegInf;
+#pragma unroll
+    for (int f = 0; f < kKeys / 32; ++f)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        float x = s[f][r] * a.scale2;
+        if (edge) {
+          const int key = k0 + 32 * f + 8 * (r / 4) + 4 * hh + r % 4;
+          x = key < min(limit, nk) ? x : kNegInf;
+        }
+        s[f][r] = x;
+        top = fmaxf(top, x);
+      }
+    top = fmaxf(half_max(top), m);
+    const float base = top == kNegInf ? 0.0f : top;   // a row that has seen nothing yet
+    const float shrink = __builtin_amdgcn_exp2f(m - base);
+    m = top;
+    float sum = 0.0f;
+#pragma unroll
+    for (int f = 0; f < kKeys / 32; ++f)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        s[f][r] = __builtin_amdgcn_exp2f(s[f][r] - base);
+        sum += s[f][r];
+      }
+    l = l * shrink + sum;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) o[d][r] *= shrink;
+#pragma unroll
+    for (int ks = 0; ks < kKeys / 16; ++ks) {
+      const bf8 p = b_operand(s[ks / 2], ks % 2);
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d) o[d] = mfma(tr_frag<2 * D>(tl.v, vb, 16 * ks, d), p, o[d]);
+    }
+  }
+  if (!live) return;
+  l = half_sum(l);
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const int64_t at = ((tq0 + row) * a.H + h) * D + 4 * hh;
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      store4(a.out, at + 32 * d + 8 * i, a.out_bf16, o[d][4 * i] * inv, o[d][4 * i + 1] * inv,
+             o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv);
+  if (hh == 0) a.lse[(int64_t)h * a.Tq + tq0 + row] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : kNegInf;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_latent_attn_expanded(const moe_latent_config* cfg, int64_t B, int64_t Tq, int64_t Tk,
+                                               const uint16_t* q, const uint16_t* kv, const uint16_t* k_rope,
+                                               const int32_t* cu_q, const int32_t* cu_k, float scale,
+                                               int32_t causal, void* out, moe_dtype ot, float* lse,
+                                               void* stream) {
+  const moe_status st = check_latent(cfg);
+  if (st != MOE_OK) return st;
+  if (B < 0 || B > 0x3fffffff || Tq < 0 || Tq > 0x7fffffff || Tk < 0 || Tk > 0x7fffffff) return MOE_ERR_SHAPE;
+  if (!good_scale(scale)) return MOE_ERR_SHAPE;
+  if (ot != MOE_BF16 && ot != MOE_F32) return MOE_ERR_DTYPE;
+  if (B == 0 || Tq == 0) return MOE_OK;
+  if (!q || !cu_q || !cu_k || !out || !lse || (Tk > 0 && (!kv || !k_rope))) return MOE_ERR_NULL;
+  if (misaligned16(q) || misaligned16(kv) || misaligned16(k_rope) || misaligned16(out)) return MOE_ERR_UNSUPPORTED;
+  const int64_t grid = (Tq / kFRows + B) * cfg->n_heads;
+  if (grid > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  const ExpandedArgs a{q, kv, k_rope, cu_q, cu_k, out, lse, Tq, Tk, (int)B, cfg->n_heads, scale * kLog2e,
+                       causal != 0, ot == MOE_BF16};
+  if (cfg->nope == 128)
+    hipLaunchKernelGGL(expanded_kernel<128>, dim3((unsigned)grid), dim3(kFWaves * kWave), 0, as_stream(stream), a);
+  else
+    hipLaunchKernelGGL(expanded_kernel<64>, dim3((unsigned)grid), dim3(kFWaves * kWave), 0, as_stream(stream), a);
+  return launch_status();
+}

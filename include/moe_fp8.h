@@ -534,6 +534,135 @@ moe_status moe_grouped_ffn_fp8_backward(
     moe_dtype dxt, void* dw1, void* dw3, void* dw2, moe_dtype dwt, void* ws, size_t ws_bytes,
     void* stream);
 
+/*
+ * Latent attention ([guide] MLA snippet; [digest] MLA pseudocode): a token's keys and
+ * values are one latent vector c shared by all heads and one rotary key, [c | k_r]. Two
+ * forms of the same attention are built, both with FP32 softmax statistics and sums:
+ *   absorbed   the key and value projections are folded into the query and the output, so
+ *              all heads attend to the cached [c | k_r] rows directly (serving);
+ *   expanded   per-head keys [k_n | k_r] and values v formed from c (prefill, training),
+ *              with its backward.
+ * Sizes that are built: latent 256 or 512, rope 64, (nope, v_dim) = (64, 64) or (128, 128).
+ */
+typedef enum moe_cache_kind {
+  MOE_CACHE_BF16 = 0, /* a row is latent + rope bf16 values                              */
+  MOE_CACHE_FP8 = 1   /* a row is latent E4M3 codes, rope bf16 values and one float scale
+                         (a power of two) per 128 codes, padded to a multiple of 16 bytes */
+} moe_cache_kind;
+
+typedef struct moe_latent_config {
+  int32_t n_heads;         /* attention heads, 1..1024                                   */
+  int32_t latent;          /* R: width of the latent vector                              */
+  int32_t rope;            /* width of the rotary key                                    */
+  int32_t nope;            /* expanded form: width of a head's key without the rotary part */
+  int32_t v_dim;           /* expanded form: width of a head's value                     */
+  int32_t cache_kind;      /* moe_cache_kind of the cache                                */
+} moe_latent_config;
+
+/* Bytes of one cache row (0 for an invalid configuration). */
+size_t moe_latent_cache_row_bytes(const moe_latent_config* cfg);
+
+/*
+ * moe_latent_cache_write — writes T tokens' rows into a paged cache. With MOE_CACHE_FP8,
+ * each 128 latent values are quantised by the power-of-two rule of moe_quantize_1x128_pow2
+ * (so that a read-back value code * scale is exact in bf16); the rotary part stays bf16.
+ * FP32 input is rounded to bf16 (nearest even) where it is kept as bf16.
+ *   x      T rows of latent + rope values (xt = MOE_F32 or MOE_BF16), row t at element
+ *          t * x_stride; 16-byte aligned rows
+ *   slots  [T] int32: the cache row of each token; a negative one or one >= n_slots is
+ *          skipped. The rows of one call must be distinct.
+ *   cache  [n_slots] rows, 16-byte aligned
+ * Errors: invalid config, T < 0, n_slots < 0, x_stride < latent + rope (SHAPE); dtype;
+ * NULL pointers; misaligned x, cache or row stride (UNSUPPORTED).
+ */
+moe_status moe_latent_cache_write(const moe_latent_config* cfg, int64_t T, const void* x, moe_dtype xt,
+                                  int64_t x_stride, const int32_t* slots, void* cache, int64_t n_slots,
+                                  void* stream);
+
+/*
+ * moe_latent_cache_read — reads the rows of B sequences back as bf16, packed one sequence
+ * after another (the input of the expansion to keys and values in a chunked prefill).
+ *   cache       [n_pages * page_size] rows; position p of sequence b is row
+ *               page_table[b * max_pages + p / page_size] * page_size + p % page_size
+ *   page_table  [B, max_pages] int32
+ *   cu_rows     [B + 1] int32: output rows [cu_rows[b], cu_rows[b + 1]) are sequence b's
+ *   starts      [B] int32, the first position of each sequence, or NULL (position 0)
+ *   out         [n_out, latent + rope] bf16 bits, 16-byte aligned. Rows outside every
+ *               sequence, and rows whose position or page is out of range, are zero.
+ * Errors: as above; page_size < 1, n_pages, max_pages, n_out or B < 0 (SHAPE).
+ */
+moe_status moe_latent_cache_read(const moe_latent_config* cfg, const void* cache, int64_t n_pages,
+                                 int32_t page_size, const int32_t* page_table, int64_t B,
+                                 int64_t max_pages, const int32_t* cu_rows, const int32_t* starts,
+                                 int64_t n_out, uint16_t* out, void* stream);
+
+/*
+ * moe_latent_attn_absorbed — attention of Sq query tokens a sequence (1 when decoding, more
+ * when drafted tokens are verified) over the cached rows, causal among the Sq tokens:
+ *   s_hj = scale * q_h . [c_j | k_rj],  j < lengths[b] - (Sq - 1 - i) for query token i,
+ *   out_h = sum_j softmax(s_h)_j c_j,   lse_h = log sum_j exp s_hj.
+ * A query that sees no row gives out = 0 and lse = -inf.
+ *   q        [B, Sq, n_heads, latent + rope] bf16 bits, 16-byte aligned
+ *   lengths  [B] int32: cached rows of each sequence, the Sq tokens' own included; values
+ *            outside 0..max_pages * page_size are clamped. Rows past a length are not
+ *            read into the result, whatever they hold; a page outside 0..n_pages-1 reads
+ *            as zero rows.
+ *   scale    > 0
+ *   out      [B, Sq, n_heads, latent] (ot = BF16/F32), lse [B, Sq, n_heads] float
+ *   ws       moe_latent_attn_absorbed_workspace_bytes(cfg, B, Sq) bytes, 16-byte aligned
+ * Errors: invalid config, Sq outside 1..64, B < 0, B > 65535, page_size < 1, other sizes
+ * < 0 or max_pages * page_size >= 2^31, scale not positive and finite (SHAPE); dtype; NULL
+ * pointers; workspace; misaligned q, cache, out or ws (UNSUPPORTED).
+ */
+size_t moe_latent_attn_absorbed_workspace_bytes(const moe_latent_config* cfg, int64_t B, int32_t Sq);
+moe_status moe_latent_attn_absorbed(const moe_latent_config* cfg, int64_t B, int32_t Sq, const uint16_t* q,
+                                    const void* cache, int64_t n_pages, int32_t page_size,
+                                    const int32_t* page_table, int64_t max_pages, const int32_t* lengths,
+                                    float scale, void* out, moe_dtype ot, float* lse, void* ws,
+                                    size_t ws_bytes, void* stream);
+
+/*
+ * moe_latent_attn_expanded — attention over expanded keys and values for B packed
+ * sequences: queries [cu_q[b], cu_q[b+1]) attend to keys [cu_k[b], cu_k[b+1]),
+ *   s_hij = scale * (q_n . k_n(h, j) + q_r . k_r(j)),  out_hi = sum_j softmax_j v(h, j).
+ * causal: the last query sees every key of its sequence, each one before it one key fewer
+ * (query i of nq sees keys j <= i + nk - nq). A query that sees no key gives out = 0 and
+ * lse = -inf.
+ *   q       [Tq, n_heads, nope + rope] bf16 bits
+ *   kv      [Tk, n_heads, nope + v_dim] bf16 bits: [k_n | v] of each head, as one
+ *           projection of the latents writes them
+ *   k_rope  [Tk, rope] bf16 bits, shared by the heads
+ *   cu_q, cu_k  [B + 1] int32, non-decreasing from 0 to at most Tq and Tk
+ *   out     [Tq, n_heads, v_dim] (ot = BF16/F32), lse [n_heads, Tq] float; rows outside
+ *           every sequence are not written
+ * Errors: invalid config, B < 0, Tq, Tk outside 0..2^31-1, scale not positive and finite
+ * (SHAPE); dtype; NULL pointers; tensors not 16-byte aligned (UNSUPPORTED).
+ */
+moe_status moe_latent_attn_expanded(const moe_latent_config* cfg, int64_t B, int64_t Tq, int64_t Tk,
+                                    const uint16_t* q, const uint16_t* kv, const uint16_t* k_rope,
+                                    const int32_t* cu_q, const int32_t* cu_k, float scale, int32_t causal,
+                                    void* out, moe_dtype ot, float* lse, void* stream);
+
+/*
+ * moe_latent_attn_expanded_backward — gradients of moe_latent_attn_expanded for the
+ * upstream gradient dout, from the forward's inputs, out (bf16) and lse:
+ *   P = exp(s - lse), D = rowsum(dout * out), dv = P^T dout, ds = P * (dout v^T - D),
+ *   dq = scale * ds k, dk = scale * ds^T q; the rotary part of dk is summed over the heads.
+ * Deterministic (no atomics).
+ *   dq [Tq, n_heads, nope + rope], dkv [Tk, n_heads, nope + v_dim], dk_rope [Tk, rope]
+ *           (gt = BF16/F32); rows outside every sequence are not written
+ *   ws      moe_latent_attn_expanded_backward_workspace_bytes(cfg, Tq, Tk) bytes
+ * Errors: as the forward; workspace.
+ */
+size_t moe_latent_attn_expanded_backward_workspace_bytes(const moe_latent_config* cfg, int64_t Tq,
+                                                         int64_t Tk);
+moe_status moe_latent_attn_expanded_backward(const moe_latent_config* cfg, int64_t B, int64_t Tq, int64_t Tk,
+                                             const uint16_t* q, const uint16_t* kv, const uint16_t* k_rope,
+                                             const int32_t* cu_q, const int32_t* cu_k, float scale,
+                                             int32_t causal, const uint16_t* out, const float* lse,
+                                             const uint16_t* dout, void* dq, void* dkv, void* dk_rope,
+                                             moe_dtype gt, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,6 +16,8 @@ Each function cites the passage it follows, by page title and section:
     accumulation; section 5.5: the per-sequence allocation entropy);
   * the zhihu infra commentary on the report (training part: E4M3 everywhere,
     1x128 / 128x128 groups, GEMM by partial-sum promotion; SwiGLU recomputed);
+  * for the latent attention (``latent.py``): the guide's and the digest's MLA passages
+    (keys and values from one cached latent vector a token, a shared rotary key);
   * for the backward (``backward.py``): the guide's [fp8] block (gemm_dgrad and
     gemm_wgrad in FP8, moe_gating kept in BF16/FP32) and the zhihu commentary (E4M3 in
     both directions).
@@ -34,6 +36,7 @@ from .backward import (  # noqa: F401
     silu_grad,
 )
 from .e4m3 import E4M3_MAX, decode, encode, finite_values  # noqa: F401
+from . import latent  # noqa: F401
 from .moe import (  # noqa: F401
     bias_update,
     combine,
