@@ -174,6 +174,13 @@ __device__ __forceinline__ void tile_copy(__amdgpu_buffer_rsrc_t src, int stride
   }
 }
 
+// Waits for this wave's own vector-memory and LDS operations.
+__device__ __forceinline__ void copies_done() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0), no export wait
+  asm volatile("" ::: "memory");
+}
+
 // Every wave of the workgroup waits for its own vector-memory and LDS operations, then for
 // the others.
 __device__ __forceinline__ void copies_done_barrier() {

@@ -139,13 +139,55 @@ __device__ __forceinline__ void store_rows(const Stage<R, WT, true>& g, LatentTi
   }
 }
 
+// E4M3 rows by way of LDS (one tile a step): a wave copies its rows' codes there one step
+// ahead of the conversion, so no register waits on memory across the products.
+template <int R>
+struct __attribute__((aligned(16))) CodeTile {
+  uint8_t row[kTok][fp8_row_bytes(R)];
+};
+
+template <int R>
+__device__ __forceinline__ void copy_codes(const AbsorbedArgs& a, CodeTile<R>* t, int slots, int wave, int lane) {
+  constexpr int kRows = kTok / kAWaves, kBytes = fp8_row_bytes(R);
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    const int slot = __builtin_amdgcn_readlane(slots, j);
+    const auto row = buffer_of(a.cache + (int64_t)max(slot, 0) * kBytes, slot >= 0 ? kBytes : 0);
+    if (lane < kBytes / 16)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(row, (lds_byte*)t->row[wave * kRows + j], 16, lane * 16, 0, 0, 0);
+  }
+}
+
+template <int R>
+__device__ __forceinline__ void convert_codes(const CodeTile<R>& g, LatentTile<R>* t, int wave, int lane) {
+  constexpr int kRows = kTok / kAWaves, kChunks = R / 16, kSide = kWave / kChunks;   // rows side by side
+#pragma unroll
+  for (int j = 0; j < kRows; j += kSide) {
+    const int r = wave * kRows + j + lane / kChunks, c = lane % kChunks;
+    const u4 v = *reinterpret_cast<const u4*>(g.row[r] + c * 16);
+    const float s = *reinterpret_cast<const float*>(g.row[r] + R + 2 * kRope + 4 * (c / 8));
+    *reinterpret_cast<u4*>(t->c + latent_off<R>(r, 2 * c)) = unpack_fp8(make_uint2(v[0], v[1]), s);
+    *reinterpret_cast<u4*>(t->c + latent_off<R>(r, 2 * c + 1)) = unpack_fp8(make_uint2(v[2], v[3]), s);
+  }
+  if (lane < kRows * 8) {
+    const int r = wave * kRows + lane / 8;
+    *reinterpret_cast<u4*>(t->r + tile_off<2 * kRope>(r, lane % 8)) =
+        *reinterpret_cast<const u4*>(g.row[r] + R + (lane % 8) * 16);
+  }
+}
+
 template <int R, int WQ, int WT, int WD, bool FP8>
 __global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedArgs a) {
   static_assert(WQ * WT * WD == kAWaves, "waves");
   constexpr int kSteps = (R + kRope) / 32, kRows = kTok * WT / kAWaves, kStep = kTok * WT;
   constexpr int kCols = R / WD, kFrags = kCols / 16;   // kFrags is 4 or a multiple of 8
   constexpr int kQRows = 16 * WQ;
+  // Query operands of the last kQLds steps wait in LDS where the registers do not hold all.
+  constexpr int kQLds = kFrags == 32 ? 6 : 0;
   __shared__ LatentTile<R> tiles[2][WT];
+  constexpr bool kCodes = FP8 && WT == 1;
+  __shared__ CodeTile<kCodes ? R : 16> codes;
+  __shared__ bf8 qlds[kAWaves][kQLds > 0 ? kQLds : 1][kWave];
   __shared__ int64_t wsum[kAWaves];
   __shared__ int64_t found[2];   // the sequence that holds the range's first step, its first step
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -205,7 +247,7 @@ __global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedAr
 
   const int M = a.Sq * a.H;
   // lane offsets of the tile reads: rows of scores, transposed rows of values
-  const int cb = latent_off<R>(col, grp);
+  const int cb = latent_off<R>(col, grp), rb = tile_off<2 * kRope>(col, grp);
   // (this wave's value columns start at column block wd * kFrags)
   const int ct = (latent_off<R>(4 * grp + (col >> 2), (col & 3) >> 1) + ((col & 1) << 3)) ^ ((wd * kFrags & 7) << 5);
   for (int64_t at = start; at < end;) {
@@ -225,11 +267,14 @@ __global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedAr
     // rows that this lane's query sees
     const int limit = len - (a.Sq - 1 - min(row, M - 1) / a.H);
 
-    bf8 qf[kSteps];
+    bf8 qf[kSteps - kQLds];
     {
       const uint16_t* qp = a.q + ((int64_t)b * M + min(row, M - 1)) * (R + kRope) + 8 * grp;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) qf[s] = *reinterpret_cast<const bf8*>(qp + 32 * s);
+      for (int s = 0; s < kSteps - kQLds; ++s) qf[s] = *reinterpret_cast<const bf8*>(qp + 32 * s);
+#pragma unroll
+      for (int s = 0; s < kQLds; ++s)
+        qlds[wave][s][lane] = *reinterpret_cast<const bf8*>(qp + 32 * (kSteps - kQLds + s));
     }
     f4 o[kFrags];
 #pragma unroll
@@ -239,30 +284,46 @@ __global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedAr
     Stage<R, WT, FP8> stage;
     const int mine = wave * kRows + min(lane, kRows - 1);
     int slots = row_slot(a, b, t0 * kStep + mine, len);
-    load_rows<R, WT, FP8>(a, stage, tiles[t0 & 1], slots, wave, lane);
-    if constexpr (FP8) store_rows<R, WT>(stage, tiles[t0 & 1], wave, lane);
-    slots = row_slot(a, b, (t0 + 1) * kStep + mine, len);
+    if constexpr (kCodes) {
+      copy_codes<R>(a, &codes, slots, wave, lane);
+      slots = row_slot(a, b, (t0 + 1) * kStep + mine, len);
+      copies_done();
+      convert_codes<R>(codes, tiles[t0 & 1], wave, lane);
+      copies_done();
+      if (t0 + 1 < t1) copy_codes<R>(a, &codes, slots, wave, lane);
+      slots = row_slot(a, b, (t0 + 2) * kStep + mine, len);
+    } else {
+      load_rows<R, WT, FP8>(a, stage, tiles[t0 & 1], slots, wave, lane);
+      if constexpr (FP8) store_rows<R, WT>(stage, tiles[t0 & 1], wave, lane);
+      slots = row_slot(a, b, (t0 + 1) * kStep + mine, len);
+    }
     for (int t = t0; t < t1; ++t) {
       copies_done_barrier();
       LatentTile<R>* next = tiles[(t + 1) & 1];
-      if (t + 1 < t1) load_rows<R, WT, FP8>(a, stage, next, slots, wave, lane);
-      if (t + 2 < t1) slots = row_slot(a, b, (t + 2) * kStep + mine, len);
+      if constexpr (kCodes) {
+        if (t + 1 < t1) convert_codes<R>(codes, next, wave, lane);
+        if (t + 2 < t1) {
+          copies_done();   // the codes are read before the next ones land on them
+          copy_codes<R>(a, &codes, slots, wave, lane);
+          slots = row_slot(a, b, (t + 3) * kStep + mine, len);
+        }
+      } else {
+        if (t + 1 < t1) load_rows<R, WT, FP8>(a, stage, next, slots, wave, lane);
+        if (t + 2 < t1) slots = row_slot(a, b, (t + 2) * kStep + mine, len);
+      }
       const LatentTile<R>& tl = tiles[t & 1][wt];
       const int p0 = t * kStep + wt * kTok;   // position of the tile's first row
       if (busy && p0 < len) {
-        f4 s[2];
+        f4 s[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          s[f] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < kSteps; ++i) {
+          const bf8 q = i < kSteps - kQLds ? qf[i < kSteps - kQLds ? i : 0]
+                                           : qlds[wave][i < kSteps - kQLds ? 0 : i - (kSteps - kQLds)][lane];
 #pragma unroll
-          for (int i = 0; i < R / 32; ++i) {
-            const bf8 k = *reinterpret_cast<const bf8*>(tl.c + f * 16 * 2 * R + (i >> 2) * 256 + (cb ^ ((i & 3) << 6)));
-            s[f] = mfma16(k, qf[i], s[f]);
-          }
-#pragma unroll
-          for (int i = 0; i < kRope / 32; ++i) {
-            const bf8 k = *reinterpret_cast<const bf8*>(tl.r + tile_off<2 * kRope>(16 * f + col, 4 * i + grp));
-            s[f] = mfma16(k, qf[R / 32 + i], s[f]);
+          for (int f = 0; f < 2; ++f) {
+            const uint8_t* k = i < R / 32 ? tl.c + f * 16 * 2 * R + (i >> 2) * 256 + (cb ^ ((i & 3) << 6))
+                                          : tl.r + f * 16 * 2 * kRope + (rb ^ ((i - R / 32) << 6));
+            s[f] = mfma16(*reinterpret_cast<const bf8*>(k), q, s[f]);
           }
         }
         const bool edge = p0 + kTok > len - (a.Sq - 1);
@@ -307,7 +368,7 @@ __global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedAr
           o[d] = mfma16(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), p.v, o[d]);
         }
       }
-      if constexpr (FP8) {
+      if constexpr (FP8 && !kCodes) {
         if (t + 1 < t1) store_rows<R, WT>(stage, next, wave, lane);
       }
     }
@@ -416,7 +477,7 @@ void launch_rows(const AbsorbedArgs& a, bool fp8, hipStream_t s) {
   switch (query_rows(a.Sq * a.H)) {
     case 16: return launch_absorbed<R, 1, 2, 4>(a, fp8, s);
     case 32: return launch_absorbed<R, 2, 2, 2>(a, fp8, s);
-    case 64: return launch_absorbed<R, 4, 2, 1>(a, fp8, s);
+    case 64: return launch_absorbed<R, 4, 1, 2>(a, fp8, s);
     default: return launch_absorbed<R, 8, 1, 1>(a, fp8, s);
   }
 }
