@@ -134,12 +134,15 @@ __device__ __forceinline__ bf8 tr_frag(const uint8_t* t, int base, int r0, int d
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// A value that all lanes hold alike, in scalar registers.
+__device__ __forceinline__ int64_t wave_uniform64(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
 template <typename T>
 __device__ __forceinline__ T* wave_uniform(T* p) {
-  const uint64_t v = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
-  return reinterpret_cast<T*>(((uint64_t)hi << 32) | lo);
+  return reinterpret_cast<T*>(wave_uniform64(reinterpret_cast<int64_t>(p)));
 }
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, int64_t bytes) {

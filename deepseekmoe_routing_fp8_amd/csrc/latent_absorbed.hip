@@ -25,6 +25,8 @@ constexpr int kAWaves = 8;
 constexpr int kAThreads = kAWaves * kWave;
 constexpr int kGroups = 256;    // workgroups: one a CU
 constexpr int kMinSteps = 2;    // steps a range holds at least
+constexpr int kAhead = 3;         // depth steps whose rows are read ahead
+constexpr float kSlack = 8.0f;  // how far (log2) a score may pass the reference of its row
 
 struct AbsorbedArgs {
   const uint16_t* q;
@@ -74,14 +76,16 @@ struct Stage {
   float s[FP8 ? kRows : 1];
 };
 
-// The cache row of position pos of sequence b, -1 if there is none.
-__device__ __forceinline__ int row_slot(const AbsorbedArgs& a, int b, int pos, int len) {
-  int slot = -1;
-  if (pos < len) {
-    const int pg = a.table[(int64_t)b * a.max_pages + pos / a.page];
-    if (pg >= 0 && pg < a.n_pages) slot = pg * a.page + pos % a.page;
-  }
-  return slot;
+// The page of position pos of sequence b as the table has it (the table's last column for a
+// position past it); a row number is formed from it a step later, when it has arrived.
+__device__ __forceinline__ int page_of(const AbsorbedArgs& a, int b, int pos) {
+  const int64_t p = min((int64_t)((uint32_t)pos / (uint32_t)a.page), a.max_pages - 1);
+  return a.table[(int64_t)b * a.max_pages + p];
+}
+// The cache row of position pos, -1 if there is none.
+__device__ __forceinline__ int row_slot(const AbsorbedArgs& a, int pg, int pos, int len) {
+  const bool there = pos < len && pg >= 0 && pg < a.n_pages;
+  return there ? pg * a.page + (int)((uint32_t)pos % (uint32_t)a.page) : -1;
 }
 
 // slots: lane j < kRows holds the cache row of the wave's j-th row.
@@ -183,7 +187,7 @@ __global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedAr
   constexpr int kCols = R / WD, kFrags = kCols / 16;   // kFrags is 4 or a multiple of 8
   constexpr int kQRows = 16 * WQ;
   // Query operands of the last kQLds steps wait in LDS where the registers do not hold all.
-  constexpr int kQLds = kFrags == 32 ? 6 : 0;
+  constexpr int kQLds = kFrags == 32 ? 8 : 0;
   __shared__ LatentTile<R> tiles[2][WT];
   constexpr bool kCodes = FP8 && WT == 1;
   __shared__ CodeTile<kCodes ? R : 16> codes;
@@ -205,7 +209,7 @@ __global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedAr
   total = 0;
 #pragma unroll
   for (int w = 0; w < kAWaves; ++w) total += wsum[w];
-  total *= a.blocks;
+  total = wave_uniform64(total) * a.blocks;
   const int64_t per = range_steps(total);
   const int64_t start = blockIdx.x * per, end = min(total, start + per);
   int64_t before = 0;
@@ -242,8 +246,8 @@ __global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedAr
   }
   __syncthreads();
   if (start >= total) return;
-  int b = (int)found[0];
-  int64_t seq0 = found[1];
+  int b = (int)wave_uniform64(found[0]);
+  int64_t seq0 = wave_uniform64(found[1]);
 
   const int M = a.Sq * a.H;
   // lane offsets of the tile reads: rows of scores, transposed rows of values
@@ -283,49 +287,50 @@ __global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedAr
 
     Stage<R, WT, FP8> stage;
     const int mine = wave * kRows + min(lane, kRows - 1);
-    int slots = row_slot(a, b, t0 * kStep + mine, len);
-    if constexpr (kCodes) {
-      copy_codes<R>(a, &codes, slots, wave, lane);
-      slots = row_slot(a, b, (t0 + 1) * kStep + mine, len);
-      copies_done();
-      convert_codes<R>(codes, tiles[t0 & 1], wave, lane);
-      copies_done();
-      if (t0 + 1 < t1) copy_codes<R>(a, &codes, slots, wave, lane);
-      slots = row_slot(a, b, (t0 + 2) * kStep + mine, len);
-    } else {
-      load_rows<R, WT, FP8>(a, stage, tiles[t0 & 1], slots, wave, lane);
-      if constexpr (FP8) store_rows<R, WT>(stage, tiles[t0 & 1], wave, lane);
-      slots = row_slot(a, b, (t0 + 1) * kStep + mine, len);
-    }
-    for (int t = t0; t < t1; ++t) {
-      copies_done_barrier();
-      LatentTile<R>* next = tiles[(t + 1) & 1];
+    auto pos_of = [&](int t) { return t * kStep + mine; };
+    // The copies of step t + 1 go to `next` while `cur` is worked on: the pointers are
+    // declared not to alias, or the reads of `cur` would wait for them.
+    auto step = [&](const LatentTile<R>* __restrict__ cur, LatentTile<R>* __restrict__ next, int t,
+                    int& pg) __attribute__((always_inline)) {
       if constexpr (kCodes) {
         if (t + 1 < t1) convert_codes<R>(codes, next, wave, lane);
         if (t + 2 < t1) {
           copies_done();   // the codes are read before the next ones land on them
-          copy_codes<R>(a, &codes, slots, wave, lane);
-          slots = row_slot(a, b, (t + 3) * kStep + mine, len);
+          copy_codes<R>(a, &codes, row_slot(a, pg, pos_of(t + 2), len), wave, lane);
+          pg = page_of(a, b, pos_of(t + 3));
         }
       } else {
-        if (t + 1 < t1) load_rows<R, WT, FP8>(a, stage, next, slots, wave, lane);
-        if (t + 2 < t1) slots = row_slot(a, b, (t + 2) * kStep + mine, len);
+        if (t + 1 < t1) load_rows<R, WT, FP8>(a, stage, next, row_slot(a, pg, pos_of(t + 1), len), wave, lane);
+        if (t + 2 < t1) pg = page_of(a, b, pos_of(t + 2));
       }
-      const LatentTile<R>& tl = tiles[t & 1][wt];
+      const LatentTile<R>& tl = cur[wt];
       const int p0 = t * kStep + wt * kTok;   // position of the tile's first row
       if (busy && p0 < len) {
         f4 s[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+        // Row reads run kAhead products' worth ahead; the scheduling barriers keep them
+        // there (left alone, every product waits for its own read).
+        auto row_at = [&](int i, int f) {
+          const uint8_t* k = i < R / 32 ? tl.c + f * 16 * 2 * R + (i >> 2) * 256 + (cb ^ ((i & 3) << 6))
+                                        : tl.r + f * 16 * 2 * kRope + (rb ^ ((i - R / 32) << 6));
+          return *reinterpret_cast<const bf8*>(k);
+        };
+        auto q_at = [&](int i) { return i < kSteps - kQLds ? qf[i] : qlds[wave][i - (kSteps - kQLds)][lane]; };
+        bf8 kf[kAhead][2], qn[2] = {q_at(0), q_at(1)};
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) kf[i][0] = row_at(i, 0), kf[i][1] = row_at(i, 1);
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
-          const bf8 q = i < kSteps - kQLds ? qf[i < kSteps - kQLds ? i : 0]
-                                           : qlds[wave][i < kSteps - kQLds ? 0 : i - (kSteps - kQLds)][lane];
-#pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            const uint8_t* k = i < R / 32 ? tl.c + f * 16 * 2 * R + (i >> 2) * 256 + (cb ^ ((i & 3) << 6))
-                                          : tl.r + f * 16 * 2 * kRope + (rb ^ ((i - R / 32) << 6));
-            s[f] = mfma16(*reinterpret_cast<const bf8*>(k), q, s[f]);
+          __builtin_amdgcn_sched_barrier(0);
+          const bf8 q = qn[i % 2];
+          s[0] = mfma16(kf[i % kAhead][0], q, s[0]);
+          s[1] = mfma16(kf[i % kAhead][1], q, s[1]);
+          if (i + 2 < kSteps) qn[i % 2] = q_at(i + 2);
+          if (i + kAhead < kSteps) {
+            kf[i % kAhead][0] = row_at(i + kAhead, 0);
+            kf[i % kAhead][1] = row_at(i + kAhead, 1);
           }
         }
+        __builtin_amdgcn_sched_barrier(0);
         const bool edge = p0 + kTok > len - (a.Sq - 1);
         float top = kNegInf;
 #pragma unroll
@@ -338,39 +343,72 @@ __global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedAr
             top = fmaxf(top, x);
           }
         top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(half_max(top), m);
-        const float base = top == kNegInf ? 0.0f : top;
-        const float shrink = __builtin_amdgcn_exp2f(m - base);
-        m = top;
-        float sum = 0.0f;
+        top = half_max(top);
+        // The running reference moves only when a score passes it by kSlack: the weights
+        // stay below 2^kSlack, exact in FP32's and bf16's range, and the sums are seldom
+        // rescaled. The first score of a row always sets it.
+        const bool moved = top > m + kSlack || (m == kNegInf && top > kNegInf);
+        if (__any(moved)) {
+          const float to = moved ? top : m;
+          const float shrink = to == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+          m = to;
+          l *= shrink;
+#pragma unroll
+          for (int d = 0; d < kFrags; ++d) o[d] *= shrink;
+        }
+        const float base = m == kNegInf ? 0.0f : m;
 #pragma unroll
         for (int f = 0; f < 2; ++f)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             s[f][r] = __builtin_amdgcn_exp2f(s[f][r] - base);
-            sum += s[f][r];
+            l += s[f][r];
           }
-        l = l * shrink + sum;
-        if (__any(shrink != 1.0f)) {
-#pragma unroll
-          for (int d = 0; d < kFrags; ++d) o[d] *= shrink;
-        }
         union { uint32_t u[4]; bf8 v; } p;
 #pragma unroll
         for (int i = 0; i < 4; ++i) p.u[i] = pack_bf16x2(s[i / 2][2 * (i % 2)], s[i / 2][2 * (i % 2) + 1]);
-#pragma unroll
-        for (int d = 0; d < kFrags; ++d) {
+        auto col_at = [&](int d) {
           // columns 16 (wd * kFrags + d)..: 4 rows a 16-lane group, of both 16-row halves
           typedef __attribute__((address_space(3))) bf4 lds_bf4;
           const uint8_t* v = tl.c + ((wd * kFrags >> 3) + (d >> 3)) * 256 + (ct ^ ((d & 7) << 5));
           const bf4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf4*)v);
           const bf4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf4*)(v + 16 * 2 * R));
-          o[d] = mfma16(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), p.v, o[d]);
+          return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        };
+        constexpr int kVAhead = kFrags < 6 ? kFrags : 6;
+        bf8 vf[kVAhead];
+#pragma unroll
+        for (int d = 0; d < kVAhead; ++d) vf[d] = col_at(d);
+#pragma unroll
+        for (int d = 0; d < kFrags; ++d) {
+          __builtin_amdgcn_sched_barrier(0);
+          o[d] = mfma16(vf[d % kVAhead], p.v, o[d]);
+          if (d + kVAhead < kFrags) vf[d % kVAhead] = col_at(d + kVAhead);
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
       if constexpr (FP8 && !kCodes) {
         if (t + 1 < t1) store_rows<R, WT>(stage, next, wave, lane);
       }
+    };
+
+    int pg = page_of(a, b, pos_of(t0));
+    if constexpr (kCodes) {
+      copy_codes<R>(a, &codes, row_slot(a, pg, pos_of(t0), len), wave, lane);
+      pg = page_of(a, b, pos_of(t0 + 1));
+      copies_done();
+      convert_codes<R>(codes, tiles[t0 & 1], wave, lane);
+      copies_done();
+      if (t0 + 1 < t1) copy_codes<R>(a, &codes, row_slot(a, pg, pos_of(t0 + 1), len), wave, lane);
+      pg = page_of(a, b, pos_of(t0 + 2));
+    } else {
+      load_rows<R, WT, FP8>(a, stage, tiles[t0 & 1], row_slot(a, pg, pos_of(t0), len), wave, lane);
+      if constexpr (FP8) store_rows<R, WT>(stage, tiles[t0 & 1], wave, lane);
+      pg = page_of(a, b, pos_of(t0 + 1));
+    }
+    for (int t = t0; t < t1; ++t) {
+      copies_done_barrier();
+      step(tiles[t & 1], tiles[(t + 1) & 1], t, pg);
     }
     l += __shfl_xor(l, 16);
     l = half_sum(l);
