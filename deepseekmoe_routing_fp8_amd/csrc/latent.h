@@ -98,11 +98,14 @@ __device__ __forceinline__ u4 unpack_fp8(uint2 q, float s) {
 // one CU: 196 bytes a clock so permuted, 120 with an 8-chunk permutation.
 __device__ __forceinline__ constexpr int row_key(int r) { return ((r & 3) << 2) | ((r >> 2) & 3); }
 // Chunk c of row r sits at chunk c ^ row_key(r) of its 256 bytes; two 128-byte rows share
-// one 256-byte line.
+// one 256-byte line, permuted by line_key (which also suits reads of 16 rows at 4 chunks).
+__device__ __forceinline__ constexpr int line_key(int line) {
+  return ((line & 1) << 2) | ((((line >> 1) ^ (line >> 2)) & 1) << 1) | ((line >> 2) & 1);
+}
 template <int W>
 __device__ __forceinline__ int tile_off(int r, int c) {
   if constexpr (W >= 256) return r * W + ((c ^ row_key(r)) << 4);
-  else return (r >> 1) * 256 + (((((r & 1) << 3) | c) ^ ((((r >> 1) & 1) << 2) | ((r >> 2) & 3))) << 4);
+  else return (r >> 1) * 256 + (((((r & 1) << 3) | c) ^ line_key(r >> 1)) << 4);
 }
 
 // A operand (32 rows x 16 depth) from a tile whose rows are the operand's rows r0 + l % 32
@@ -127,10 +130,11 @@ __device__ __forceinline__ int tr_base(int lane) {
 template <int W>
 __device__ __forceinline__ bf8 tr_frag(const uint8_t* t, int base, int r0, int d) {
   typedef __attribute__((address_space(3))) bf4 lds_bf4;
+  constexpr int kHi = W >= 256 ? 32 : 48;   // what 8 rows on change in the permutation
   const uint8_t* p = t + (d >> 2) * 256;
   const bf4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf4*)(p + r0 * W + (base ^ ((d & 3) << 6))));
   const bf4 hi =
-      __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf4*)(p + (r0 + 8) * W + (base ^ (((d & 3) << 6) | 32))));
+      __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf4*)(p + (r0 + 8) * W + (base ^ (((d & 3) << 6) | kHi))));
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
@@ -168,7 +172,7 @@ __device__ __forceinline__ void tile_copy(__amdgpu_buffer_rsrc_t src, int stride
       r = line;
       c = pos ^ row_key(line);
     } else {
-      const int x = pos ^ (((line & 1) << 2) | ((line >> 1) & 3));
+      const int x = pos ^ line_key(line);
       r = 2 * line + (x >> 3);
       c = x & 7;
     }

@@ -56,9 +56,14 @@ __device__ __forceinline__ int64_t range_steps(int64_t total) {
 __host__ __device__ constexpr int64_t part_floats(int latent, int n) { return (int64_t)n * (latent + 2); }
 
 // LDS tile of cached rows. Latent rows: 16-byte chunk c of row r at chunk c ^ latent_key(r)
-// of its 256 bytes, so that 16 rows at one chunk (ds_read_b128) and 8 rows at 2 adjacent
-// chunks (transposed reads of 16 columns) touch each of the 64 banks once.
-__device__ __forceinline__ constexpr int latent_key(int r) { return ((r & 7) << 1) | ((r >> 3) & 1); }
+// of its 256 bytes. A read of 16 rows at 4 chunks (ds_read_b128) is served in quarters of
+// lanes 0-3, 12-15, 20-27 and the like: rows 0-3 and 12-15 of one chunk with rows 4-11 of
+// the next; transposed reads take 8 rows at 2 adjacent chunks. With this key both touch
+// each of the 64 banks once (with (r & 7) << 1 | r >> 3, quarters collided: a third of the
+// LDS cycles).
+__device__ __forceinline__ constexpr int latent_key(int r) {
+  return (((r & 7) ^ ((r & 8) >> 1)) << 1) | ((r >> 3) & 1);
+}
 template <int R>
 __device__ __forceinline__ int latent_off(int r, int c) { return r * 2 * R + ((c ^ latent_key(r)) << 4); }
 
@@ -116,7 +121,7 @@ __device__ __forceinline__ void load_rows(const AbsorbedArgs& a, Stage<R, WT, FP
     // rotary keys: lane l stages the 16 bytes at l * 16 of the wave's 128-byte rows
     if (lane < kRows * 8) {
       const int line = row0 / 2 + (lane >> 4);
-      const int x = (lane & 15) ^ (((line & 1) << 2) | ((line >> 1) & 3));
+      const int x = (lane & 15) ^ line_key(line);
       const int slot = __shfl(slots, 2 * line + (x >> 3) - row0);
       uint8_t* to = t->r + row0 * 128;
       if (slot >= 0)
