@@ -630,28 +630,50 @@ def moe_grouped_ffn_fp8_backward(cfg: moe_config, n_experts: int, xq, xs, x, row
 # ---------------------------------------------------------------------------------------
 # Latent attention
 # ---------------------------------------------------------------------------------------
-def _same_device(*tensors):
-    """The tensors' device; they have to share it, and it has to be the current one (the
-    library launches there)."""
-    dev = tensors[0].device
-    for t in tensors[1:]:
-        if t is not None and t.device != dev:
-            raise MoEError(f"tensors on different devices: {dev} and {t.device}")
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise MoEError(f"tensors on {dev}, which is not the current device")
+# A decoding step's calls take a few microseconds on the GPU, so these functions check each
+# tensor once and cheaply (a launch costs 3 us of host time; a step by step check of every
+# property with the public stream query cost 7 us more).
+def _device_of(t, name: str) -> int:
+    """Index of the tensor's device, which has to be the current one (the library launches
+    there)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise MoEError(f"{name} must be a device tensor")
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise MoEError(f"{name} is on device {dev}, the current one is {torch.cuda.current_device()}")
     return dev
 
 
-def _new(shape, dtype, dev, stream):
+def _stream_on(dev: int, stream) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _ptr(t, dtype, shape, dev: int, name: str) -> int:
+    """Address of a contiguous tensor of this dtype and shape on device ``dev``."""
+    if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.get_device() == dev
+            and t.is_contiguous()):
+        return t.data_ptr()
+    _dev(t, dtype, name, shape)
+    raise MoEError(f"{name} is on {t.device}, the other tensors on device {dev}")
+
+
+def _new(shape, dtype, dev: int, stream):
     """A tensor for a call on ``stream``: memory of torch's current stream, kept until the
     other stream is done with it."""
-    t = torch.empty(shape, dtype=dtype, device=dev)
+    t = torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
     if stream is not None:
         t.record_stream(stream)
     return t
 
 
-def _dim(t, n: int, name: str):
+def _workspace(ws, need: int, dev: int, stream):
+    """(tensor, address, bytes) of a workspace, allocated when None."""
+    if ws is None:
+        ws = _new((max(need, 1),), torch.uint8, dev, stream)
+    return ws, _ptr(ws, torch.uint8, (ws.numel(),), dev, "ws"), ws.numel()
+
+
+def _dims(t, n: int, name: str):
     if not isinstance(t, torch.Tensor) or t.dim() != n:
         raise MoEError(f"{name} must be a tensor of {n} dimensions")
     return t.shape
@@ -661,15 +683,14 @@ def moe_latent_cache_row_bytes(cfg: moe_latent_config) -> int:
     return int(_lib.moe_latent_cache_row_bytes(ctypes.byref(cfg)))
 
 
-def _cache_args(cfg, cache):
-    """Pointer, pages and page size of a cache [n_pages, page_size, row]: uint8 rows of
+def _cache_args(cfg, cache, dev: int):
+    """Address, pages and page size of a cache [n_pages, page_size, row]: uint8 rows of
     moe_latent_cache_row_bytes bytes, or bf16 rows for a bf16 cache."""
-    n_pages, page, _ = _dim(cache, 3, "cache")
+    n_pages, page, _ = _dims(cache, 3, "cache")
     if cfg.cache_kind == MOE_CACHE_BF16:
-        p = _dev(cache, torch.bfloat16, "cache", (n_pages, page, cfg.latent + cfg.rope))
-    else:
-        p = _dev(cache, torch.uint8, "cache", (n_pages, page, moe_latent_cache_row_bytes(cfg)))
-    return p, n_pages, page
+        return _ptr(cache, torch.bfloat16, (n_pages, page, cfg.latent + cfg.rope), dev, "cache"), n_pages, page
+    row = moe_latent_cache_row_bytes(cfg)
+    return _ptr(cache, torch.uint8, (n_pages, page, row), dev, "cache"), n_pages, page
 
 
 def moe_latent_cache_write(cfg: moe_latent_config, x: torch.Tensor, slots: torch.Tensor, cache: torch.Tensor,
@@ -677,16 +698,18 @@ def moe_latent_cache_write(cfg: moe_latent_config, x: torch.Tensor, slots: torch
     """Writes the tokens' rows x [T, latent + rope] (bf16 or f32; rows may be strided, as a
     slice of a wider projection is) into cache rows ``slots`` [T] int32 (page * page_size +
     offset; negative: skipped; distinct). Returns cache."""
-    T, W = _dim(x, 2, "x")
-    _same_device(x, slots, cache)
+    dev = _device_of(x, "x")
+    T, W = _dims(x, 2, "x")
     if W != cfg.latent + cfg.rope:
         raise MoEError(f"x must have {cfg.latent + cfg.rope} columns, got {W}")
-    if W > 0 and x.stride(1) != 1:
+    row, col = x.stride()
+    if col != 1:
         raise MoEError("the columns of x must be contiguous")
-    ptr, n_pages, page = _cache_args(cfg, cache)
+    ptr, n_pages, page = _cache_args(cfg, cache, dev)
     _check(_lib.moe_latent_cache_write(
-        ctypes.byref(cfg), T, ctypes.c_void_p(x.data_ptr()), _xdtype(x), x.stride(0) if T > 1 else W,
-        _dev(slots, torch.int32, "slots", (T,)), ptr, n_pages * page, _stream(stream)), "moe_latent_cache_write")
+        ctypes.byref(cfg), T, x.data_ptr(), _xdtype(x), row if T > 1 else W,
+        _ptr(slots, torch.int32, (T,), dev, "slots"), ptr, n_pages * page, _stream_on(dev, stream)),
+        "moe_latent_cache_write")
     return cache
 
 
@@ -695,18 +718,20 @@ def moe_latent_cache_read(cfg: moe_latent_config, cache: torch.Tensor, page_tabl
                           n_out: int = None, stream=None) -> torch.Tensor:
     """-> out [n_out, latent + rope] bf16: rows cu_rows[b]..cu_rows[b+1] are sequence b's
     positions from starts[b] (0 when None) on. Pass ``out`` or ``n_out``."""
-    B, max_pages = _dim(page_table, 2, "page_table")
-    dev = _same_device(cache, page_table, cu_rows, starts, out)
+    dev = _device_of(cache, "cache")
+    B, max_pages = _dims(page_table, 2, "page_table")
+    W = cfg.latent + cfg.rope
     if out is None:
         if n_out is None:
             raise MoEError("pass out or n_out")
-        out = _new((n_out, cfg.latent + cfg.rope), torch.bfloat16, dev, stream)
-    ptr, n_pages, page = _cache_args(cfg, cache)
-    n = _dim(out, 2, "out")[0]
+        out = _new((n_out, W), torch.bfloat16, dev, stream)
+    ptr, n_pages, page = _cache_args(cfg, cache, dev)
+    n = _dims(out, 2, "out")[0]
     _check(_lib.moe_latent_cache_read(
-        ctypes.byref(cfg), ptr, n_pages, page, _dev(page_table, torch.int32, "page_table"), B, max_pages,
-        _dev(cu_rows, torch.int32, "cu_rows", (B + 1,)), _opt(starts, torch.int32, "starts", (B,)), n,
-        _dev(out, torch.bfloat16, "out", (n, cfg.latent + cfg.rope)), _stream(stream)), "moe_latent_cache_read")
+        ctypes.byref(cfg), ptr, n_pages, page, _ptr(page_table, torch.int32, (B, max_pages), dev, "page_table"), B,
+        max_pages, _ptr(cu_rows, torch.int32, (B + 1,), dev, "cu_rows"),
+        None if starts is None else _ptr(starts, torch.int32, (B,), dev, "starts"), n,
+        _ptr(out, torch.bfloat16, (n, W), dev, "out"), _stream_on(dev, stream)), "moe_latent_cache_read")
     return out
 
 
@@ -721,33 +746,33 @@ def moe_latent_attn_absorbed(cfg: moe_latent_config, q: torch.Tensor, cache: tor
     """-> (out [B, Sq, n_heads, latent], lse [B, Sq, n_heads] f32): the absorbed form for
     q [B, Sq, n_heads, latent + rope] bf16 over the first lengths[b] cached rows of each
     sequence, causal among the Sq tokens (whose rows the length includes)."""
-    B, Sq, H, W = _dim(q, 4, "q")
-    dev = _same_device(q, cache, page_table, lengths, out, lse, ws)
+    dev = _device_of(q, "q")
+    B, Sq, _, _ = _dims(q, 4, "q")
+    H, R = cfg.n_heads, cfg.latent
     if out is None:
-        out = _new((B, Sq, H, cfg.latent), out_dtype, dev, stream)
+        out = _new((B, Sq, H, R), out_dtype, dev, stream)
     if lse is None:
         lse = _new((B, Sq, H), torch.float32, dev, stream)
-    if ws is None:
-        ws = _new((max(moe_latent_attn_absorbed_workspace_bytes(cfg, B, Sq), 1),), torch.uint8, dev, stream)
-    ptr, n_pages, page = _cache_args(cfg, cache)
-    max_pages = _dim(page_table, 2, "page_table")[1]
+    need = moe_latent_attn_absorbed_workspace_bytes(cfg, B, Sq) if ws is None else 0
+    ws, ws_ptr, ws_bytes = _workspace(ws, need, dev, stream)
+    ptr, n_pages, page = _cache_args(cfg, cache, dev)
+    max_pages = _dims(page_table, 2, "page_table")[1]
     _check(_lib.moe_latent_attn_absorbed(
-        ctypes.byref(cfg), B, Sq, _dev(q, torch.bfloat16, "q", (B, Sq, cfg.n_heads, cfg.latent + cfg.rope)),
-        ptr, n_pages, page, _dev(page_table, torch.int32, "page_table", (B, max_pages)), max_pages,
-        _dev(lengths, torch.int32, "lengths", (B,)), scale,
-        _dev(out, out.dtype, "out", (B, Sq, H, cfg.latent)), _dt(out),
-        _dev(lse, torch.float32, "lse", (B, Sq, H)), _dev(ws, torch.uint8, "ws"), ws.numel(),
-        _stream(stream)), "moe_latent_attn_absorbed")
+        ctypes.byref(cfg), B, Sq, _ptr(q, torch.bfloat16, (B, Sq, H, R + cfg.rope), dev, "q"), ptr, n_pages, page,
+        _ptr(page_table, torch.int32, (B, max_pages), dev, "page_table"), max_pages,
+        _ptr(lengths, torch.int32, (B,), dev, "lengths"), scale, _ptr(out, out.dtype, (B, Sq, H, R), dev, "out"),
+        _dt(out), _ptr(lse, torch.float32, (B, Sq, H), dev, "lse"), ws_ptr, ws_bytes, _stream_on(dev, stream)),
+        "moe_latent_attn_absorbed")
     return out, lse
 
 
-def _expanded_args(cfg, q, kv, k_rope, cu_q, cu_k, scale, causal):
-    Tq, Tk, B = _dim(q, 3, "q")[0], _dim(kv, 3, "kv")[0], _dim(cu_q, 1, "cu_q")[0] - 1
-    H = cfg.n_heads
-    return (ctypes.byref(cfg), B, Tq, Tk, _dev(q, torch.bfloat16, "q", (Tq, H, cfg.nope + cfg.rope)),
-            _dev(kv, torch.bfloat16, "kv", (Tk, H, cfg.nope + cfg.v_dim)),
-            _dev(k_rope, torch.bfloat16, "k_rope", (Tk, cfg.rope)), _dev(cu_q, torch.int32, "cu_q"),
-            _dev(cu_k, torch.int32, "cu_k", (B + 1,)), scale, int(bool(causal)))
+def _expanded_args(cfg, q, kv, k_rope, cu_q, cu_k, scale, causal, dev: int):
+    Tq, Tk, B = _dims(q, 3, "q")[0], _dims(kv, 3, "kv")[0], _dims(cu_q, 1, "cu_q")[0] - 1
+    H, D, W = cfg.n_heads, cfg.nope, cfg.rope
+    return (ctypes.byref(cfg), B, Tq, Tk, _ptr(q, torch.bfloat16, (Tq, H, D + W), dev, "q"),
+            _ptr(kv, torch.bfloat16, (Tk, H, D + cfg.v_dim), dev, "kv"),
+            _ptr(k_rope, torch.bfloat16, (Tk, W), dev, "k_rope"), _ptr(cu_q, torch.int32, (B + 1,), dev, "cu_q"),
+            _ptr(cu_k, torch.int32, (B + 1,), dev, "cu_k"), scale, 1 if causal else 0)
 
 
 def moe_latent_attn_expanded(cfg: moe_latent_config, q: torch.Tensor, kv: torch.Tensor, k_rope: torch.Tensor,
@@ -757,16 +782,16 @@ def moe_latent_attn_expanded(cfg: moe_latent_config, q: torch.Tensor, kv: torch.
     """-> (out [Tq, n_heads, v_dim], lse [n_heads, Tq] f32): the expanded form for packed
     sequences, q [Tq, n_heads, nope + rope], kv [Tk, n_heads, nope + v_dim] (key part, then
     value), k_rope [Tk, rope] bf16, offsets cu_q, cu_k [B + 1] int32."""
-    Tq, H, _ = _dim(q, 3, "q")
-    dev = _same_device(q, kv, k_rope, cu_q, cu_k, out, lse)
+    dev = _device_of(q, "q")
+    args = _expanded_args(cfg, q, kv, k_rope, cu_q, cu_k, scale, causal, dev)
+    Tq, H, D = args[2], cfg.n_heads, cfg.v_dim
     if out is None:
-        out = _new((Tq, H, cfg.v_dim), out_dtype, dev, stream)
+        out = _new((Tq, H, D), out_dtype, dev, stream)
     if lse is None:
         lse = _new((H, Tq), torch.float32, dev, stream)
     _check(_lib.moe_latent_attn_expanded(
-        *_expanded_args(cfg, q, kv, k_rope, cu_q, cu_k, scale, causal),
-        _dev(out, out.dtype, "out", (Tq, H, cfg.v_dim)), _dt(out), _dev(lse, torch.float32, "lse", (H, Tq)),
-        _stream(stream)), "moe_latent_attn_expanded")
+        *args, _ptr(out, out.dtype, (Tq, H, D), dev, "out"), _dt(out),
+        _ptr(lse, torch.float32, (H, Tq), dev, "lse"), _stream_on(dev, stream)), "moe_latent_attn_expanded")
     return out, lse
 
 
@@ -782,20 +807,19 @@ def moe_latent_attn_expanded_backward(cfg: moe_latent_config, q: torch.Tensor, k
                                       ws: torch.Tensor = None, stream=None):
     """-> (dq, dkv, dk_rope) of the shapes of q, kv, k_rope (bf16 or f32, all alike), from
     the forward's inputs, out (bf16) and lse and the upstream gradient dout (bf16)."""
-    Tq, H, _ = _dim(q, 3, "q")
-    Tk = _dim(kv, 3, "kv")[0]
-    dev = _same_device(q, kv, k_rope, cu_q, cu_k, out, lse, dout, dq, dkv, dk_rope, ws)
+    dev = _device_of(q, "q")
+    args = _expanded_args(cfg, q, kv, k_rope, cu_q, cu_k, scale, causal, dev)
+    Tq, Tk, H, D = args[2], args[3], cfg.n_heads, cfg.v_dim
     dq = _new(q.shape, grad_dtype, dev, stream) if dq is None else dq
     dkv = _new(kv.shape, dq.dtype, dev, stream) if dkv is None else dkv
     dk_rope = _new(k_rope.shape, dq.dtype, dev, stream) if dk_rope is None else dk_rope
-    if ws is None:
-        ws = _new((max(moe_latent_attn_expanded_backward_workspace_bytes(cfg, Tq, Tk), 1),), torch.uint8, dev, stream)
+    need = moe_latent_attn_expanded_backward_workspace_bytes(cfg, Tq, Tk) if ws is None else 0
+    ws, ws_ptr, ws_bytes = _workspace(ws, need, dev, stream)
     _check(_lib.moe_latent_attn_expanded_backward(
-        *_expanded_args(cfg, q, kv, k_rope, cu_q, cu_k, scale, causal),
-        _dev(out, torch.bfloat16, "out", (Tq, H, cfg.v_dim)), _dev(lse, torch.float32, "lse", (H, Tq)),
-        _dev(dout, torch.bfloat16, "dout", (Tq, H, cfg.v_dim)), _dev(dq, dq.dtype, "dq", q.shape),
-        _dev(dkv, dq.dtype, "dkv", kv.shape), _dev(dk_rope, dq.dtype, "dk_rope", k_rope.shape), _dt(dq),
-        _dev(ws, torch.uint8, "ws"), ws.numel(), _stream(stream)), "moe_latent_attn_expanded_backward")
+        *args, _ptr(out, torch.bfloat16, (Tq, H, D), dev, "out"), _ptr(lse, torch.float32, (H, Tq), dev, "lse"),
+        _ptr(dout, torch.bfloat16, (Tq, H, D), dev, "dout"), _ptr(dq, dq.dtype, q.shape, dev, "dq"),
+        _ptr(dkv, dq.dtype, kv.shape, dev, "dkv"), _ptr(dk_rope, dq.dtype, k_rope.shape, dev, "dk_rope"), _dt(dq),
+        ws_ptr, ws_bytes, _stream_on(dev, stream)), "moe_latent_attn_expanded_backward")
     return dq, dkv, dk_rope
 
 
