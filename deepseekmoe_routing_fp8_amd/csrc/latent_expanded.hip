@@ -14,13 +14,14 @@ namespace {
 constexpr int kKeys = 64;    // keys a tile
 constexpr int kFWaves = 4;   // waves of a workgroup
 constexpr int kFRows = 32 * kFWaves;
+constexpr float kSlack = 8.0f;   // how far (log2) a score may pass the reference of its row
 
 struct ExpandedArgs {
   const uint16_t *q, *kv, *kr;
   const int32_t *cu_q, *cu_k;
   void* out;
   float* lse;
-  int64_t Tq, Tk;
+  int64_t Tq, Tk, slots, per_xcd;   // tile slots of a head; (head, slot) pairs of an XCD
   int B, H;
   float scale2;   // scale * log2(e)
   int causal, out_bf16;
@@ -45,11 +46,16 @@ __device__ __forceinline__ void copy_kv(const ExpandedArgs& a, KvTile<D>* t, int
 template <int D>
 __global__ __launch_bounds__(kFWaves* kWave, 2) void expanded_kernel(const ExpandedArgs a) {
   constexpr int kSteps = (D + kRope) / 16;
-  __shared__ KvTile<D> tiles[2];
+  __shared__ KvTile<D> tile0, tile1;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, hh = lane >> 5;
-  const int h = blockIdx.x % a.H;
-  const SeqTile st = find_seq<kFRows>(a.cu_q, a.B, blockIdx.x / a.H);
+  // Workgroups go to the 8 XCDs in turn: each takes a contiguous part of the (head, tile)
+  // list, so that the tiles of a head read its keys through one L2; a head's last tiles,
+  // the longest when causal, first.
+  const int64_t id = (int64_t)(blockIdx.x & 7) * a.per_xcd + (blockIdx.x >> 3);
+  if (id >= a.slots * a.H) return;
+  const int h = (int)(id / a.slots);
+  const SeqTile st = find_seq<kFRows>(a.cu_q, a.B, a.slots - 1 - id % a.slots);
   const int64_t tq0 = min((int64_t)max(a.cu_q[st.b], 0), a.Tq);
   const int64_t tk0 = min((int64_t)max(a.cu_k[st.b], 0), a.Tk);
   const int nq = (int)(min((int64_t)a.cu_q[st.b + 1], a.Tq) - tq0);
@@ -60,7 +66,7 @@ __global__ __launch_bounds__(kFWaves* kWave, 2) void expanded_kernel(const Expan
   const int row = w0 + col;                    // this lane's query
   const bool live = row < nq;
   // keys that this lane's query sees: j < limit
-  const int limit = a.causal ? row + nk - nq + 1 : nk;
+  const int limit = a.causal ? min(nk, row + nk - nq + 1) : nk;
   const int wg_limit = a.causal ? min(nk, (int)min(q0 + kFRows, (int64_t)nq) + nk - nq) : nk;
   const int n_tiles = max(0, (wg_limit + kKeys - 1) / kKeys);
 
@@ -76,60 +82,68 @@ __global__ __launch_bounds__(kFWaves* kWave, 2) void expanded_kernel(const Expan
   float m = kNegInf, l = 0.0f;
   const int kb = row_base<2 * D>(lane), rb = row_base<2 * kRope>(lane), vb = tr_base<2 * D>(lane);
 
-  if (n_tiles > 0) copy_kv<D>(a, &tiles[0], tk0, min(kKeys, nk), h, wave, lane);
-  for (int t = 0; t < n_tiles; ++t) {
-    copies_done_barrier();
+  // The copies of tile t + 1 go to `next` while `cur` is worked on: the pointers are declared
+  // not to alias, or the transposed reads of `cur` would wait for them.
+  auto step = [&](const KvTile<D>* __restrict__ cur, KvTile<D>* __restrict__ next,
+                  int t) __attribute__((always_inline)) {
     const int k0 = t * kKeys;
-    if (t + 1 < n_tiles)
-      copy_kv<D>(a, &tiles[(t + 1) & 1], tk0 + k0 + kKeys, min(kKeys, nk - k0 - kKeys), h, wave, lane);
-    const KvTile<D>& tl = tiles[t & 1];
+    if (t + 1 < n_tiles) copy_kv<D>(a, next, tk0 + k0 + kKeys, min(kKeys, nk - k0 - kKeys), h, wave, lane);
     f16v s[kKeys / 32];
 #pragma unroll
     for (int f = 0; f < kKeys / 32; ++f) {
       s[f] = zero16();
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) s[f] = mfma(row_frag<2 * D>(tl.k, kb, 32 * f, i), qf[i], s[f]);
+      for (int i = 0; i < D / 16; ++i) s[f] = mfma(row_frag<2 * D>(cur->k, kb, 32 * f, i), qf[i], s[f]);
 #pragma unroll
       for (int i = 0; i < kRope / 16; ++i)
-        s[f] = mfma(row_frag<2 * kRope>(tl.r, rb, 32 * f, i), qf[D / 16 + i], s[f]);
+        s[f] = mfma(row_frag<2 * kRope>(cur->r, rb, 32 * f, i), qf[D / 16 + i], s[f]);
     }
-    // scores in units of log2, hidden ones at -inf
-    const bool edge = k0 + kKeys > (a.causal ? min(nk, w0 + nk - nq + 1) : nk);
+    if (k0 + kKeys > (a.causal ? min(nk, w0 + nk - nq + 1) : nk)) {   // some query hides some key
+#pragma unroll
+      for (int f = 0; f < kKeys / 32; ++f)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          s[f][r] = k0 + 32 * f + 8 * (r / 4) + 4 * hh + r % 4 < limit ? s[f][r] : kNegInf;
+    }
     float top = kNegInf;
 #pragma unroll
     for (int f = 0; f < kKeys / 32; ++f)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        float x = s[f][r] * a.scale2;
-        if (edge) {
-          const int key = k0 + 32 * f + 8 * (r / 4) + 4 * hh + r % 4;
-          x = key < min(limit, nk) ? x : kNegInf;
-        }
-        s[f][r] = x;
-        top = fmaxf(top, x);
-      }
-    top = fmaxf(half_max(top), m);
-    const float base = top == kNegInf ? 0.0f : top;   // a row that has seen nothing yet
-    const float shrink = __builtin_amdgcn_exp2f(m - base);
-    m = top;
-    float sum = 0.0f;
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[f][r]);
+    top = half_max(top) * a.scale2;
+    // The reference of a row (m, in log2) moves only when a score passes it by kSlack: the
+    // weights stay below 2^kSlack, and O is seldom rescaled. A row's first score sets it.
+    const bool moved = top > m + kSlack || (m == kNegInf && top > kNegInf);
+    if (__any(moved)) {
+      const float to = moved ? top : m;
+      const float shrink = to == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+      m = to;
+      l *= shrink;
 #pragma unroll
-    for (int f = 0; f < kKeys / 32; ++f)
+      for (int d = 0; d < D / 32; ++d)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        s[f][r] = __builtin_amdgcn_exp2f(s[f][r] - base);
-        sum += s[f][r];
-      }
-    l = l * shrink + sum;
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) o[d][r] *= shrink;
+        for (int r = 0; r < 16; ++r) o[d][r] *= shrink;
+    }
+    const float base = m == kNegInf ? 0.0f : m;
 #pragma unroll
     for (int ks = 0; ks < kKeys / 16; ++ks) {
+#pragma unroll
+      for (int r = 8 * (ks % 2); r < 8 * (ks % 2) + 8; ++r) {
+        s[ks / 2][r] = __builtin_amdgcn_exp2f(fmaf(s[ks / 2][r], a.scale2, -base));
+        l += s[ks / 2][r];
+      }
       const bf8 p = b_operand(s[ks / 2], ks % 2);
 #pragma unroll
-      for (int d = 0; d < D / 32; ++d) o[d] = mfma(tr_frag<2 * D>(tl.v, vb, 16 * ks, d), p, o[d]);
+      for (int d = 0; d < D / 32; ++d) o[d] = mfma(tr_frag<2 * D>(cur->v, vb, 16 * ks, d), p, o[d]);
+    }
+  };
+  if (n_tiles > 0) copy_kv<D>(a, &tile0, tk0, min(kKeys, nk), h, wave, lane);
+  for (int t = 0; t < n_tiles; t += 2) {   // two tiles a turn: the buffers' addresses are constants
+    copies_done_barrier();
+    step(&tile0, &tile1, t);
+    if (t + 1 < n_tiles) {
+      copies_done_barrier();
+      step(&tile1, &tile0, t + 1);
     }
   }
   if (!live) return;
@@ -163,13 +177,12 @@ extern "C" moe_status moe_latent_attn_expanded(const moe_latent_config* cfg, int
   if (B == 0 || Tq == 0) return MOE_OK;
   if (!q || !cu_q || !cu_k || !out || !lse || (Tk > 0 && (!kv || !k_rope))) return MOE_ERR_NULL;
   if (misaligned16(q) || misaligned16(kv) || misaligned16(k_rope) || misaligned16(out)) return MOE_ERR_UNSUPPORTED;
-  const int64_t grid = (Tq / kFRows + B) * cfg->n_heads;
-  if (grid > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
-  const ExpandedArgs a{q, kv, k_rope, cu_q, cu_k, out, lse, Tq, Tk, (int)B, cfg->n_heads, scale * kLog2e,
-                       causal != 0, ot == MOE_BF16};
-  if (cfg->nope == 128)
-    hipLaunchKernelGGL(expanded_kernel<128>, dim3((unsigned)grid), dim3(kFWaves * kWave), 0, as_stream(stream), a);
-  else
-    hipLaunchKernelGGL(expanded_kernel<64>, dim3((unsigned)grid), dim3(kFWaves * kWave), 0, as_stream(stream), a);
+  const int64_t slots = Tq / kFRows + B, per_xcd = (slots * cfg->n_heads + 7) / 8;
+  if (per_xcd * 8 > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  const ExpandedArgs a{q, kv, k_rope, cu_q, cu_k, out, lse, Tq, Tk, slots, per_xcd, (int)B, cfg->n_heads,
+                       scale * kLog2e, causal != 0, ot == MOE_BF16};
+  const dim3 grid((unsigned)(per_xcd * 8)), block(kFWaves * kWave);
+  if (cfg->nope == 128) hipLaunchKernelGGL(expanded_kernel<128>, grid, block, 0, as_stream(stream), a);
+  else hipLaunchKernelGGL(expanded_kernel<64>, grid, block, 0, as_stream(stream), a);
   return launch_status();
 }
