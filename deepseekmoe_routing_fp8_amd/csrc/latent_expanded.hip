@@ -43,19 +43,32 @@ __device__ __forceinline__ void copy_kv(const ExpandedArgs& a, KvTile<D>* t, int
   tile_copy<2 * D, kKeys, kFWaves>(kv, stride, 2 * D, t->v, wave, lane);
 }
 
-template <int D>
-__global__ __launch_bounds__(kFWaves* kWave, 2) void expanded_kernel(const ExpandedArgs a) {
+// PARTS = 2: a second group of waves takes every other tile of the same queries, and the
+// two join through LDS at the end. It halves the time of one workgroup, for launches whose
+// workgroups are too few to fill the card or to even out their lengths.
+template <int D, int PARTS>
+__global__ __launch_bounds__(kFWaves* PARTS* kWave, 2) void expanded_kernel(const ExpandedArgs a) {
   constexpr int kSteps = (D + kRope) / 16;
-  __shared__ KvTile<D> tile0, tile1;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  __shared__ KvTile<D> tiles[PARTS][2];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = w % kFWaves, part = w / kFWaves;
   const int col = lane & 31, hh = lane >> 5;
-  // Workgroups go to the 8 XCDs in turn: each takes a contiguous part of the (head, tile)
-  // list, so that the tiles of a head read its keys through one L2; a head's last tiles,
-  // the longest when causal, first.
-  const int64_t id = (int64_t)(blockIdx.x & 7) * a.per_xcd + (blockIdx.x >> 3);
-  if (id >= a.slots * a.H) return;
-  const int h = (int)(id / a.slots);
-  const SeqTile st = find_seq<kFRows>(a.cu_q, a.B, a.slots - 1 - id % a.slots);
+  int h;
+  int64_t slot;
+  if (PARTS == 1) {
+    // Workgroups go to the 8 XCDs in turn: each takes a contiguous part of the (head, tile)
+    // list, so that the tiles of a head read its keys through one L2; a head's last tiles,
+    // the longest when causal, first.
+    const int64_t id = (int64_t)(blockIdx.x & 7) * a.per_xcd + (blockIdx.x >> 3);
+    if (id >= a.slots * a.H) return;
+    h = (int)(id / a.slots);
+    slot = a.slots - 1 - id % a.slots;
+  } else {
+    // few: all heads' long tiles start at once
+    h = blockIdx.x % a.H;
+    slot = a.slots - 1 - blockIdx.x / a.H;
+  }
+  const SeqTile st = find_seq<kFRows>(a.cu_q, a.B, slot);
   const int64_t tq0 = min((int64_t)max(a.cu_q[st.b], 0), a.Tq);
   const int64_t tk0 = min((int64_t)max(a.cu_k[st.b], 0), a.Tk);
   const int nq = (int)(min((int64_t)a.cu_q[st.b + 1], a.Tq) - tq0);
@@ -82,12 +95,16 @@ __global__ __launch_bounds__(kFWaves* kWave, 2) void expanded_kernel(const Expan
   float m = kNegInf, l = 0.0f;
   const int kb = row_base<2 * D>(lane), rb = row_base<2 * kRope>(lane), vb = tr_base<2 * D>(lane);
 
-  // The copies of tile t + 1 go to `next` while `cur` is worked on: the pointers are declared
+  // The copies of the next tile go to `next` while `cur` is worked on: the pointers are declared
   // not to alias, or the transposed reads of `cur` would wait for them.
+  auto copy = [&](KvTile<D>* to, int t) __attribute__((always_inline)) {
+    if (t < n_tiles) copy_kv<D>(a, to, tk0 + t * kKeys, min(kKeys, nk - t * kKeys), h, wave, lane);
+  };
   auto step = [&](const KvTile<D>* __restrict__ cur, KvTile<D>* __restrict__ next,
                   int t) __attribute__((always_inline)) {
     const int k0 = t * kKeys;
-    if (t + 1 < n_tiles) copy_kv<D>(a, next, tk0 + k0 + kKeys, min(kKeys, nk - k0 - kKeys), h, wave, lane);
+    copy(next, t + PARTS);
+    if (PARTS > 1 && t >= n_tiles) return;
     f16v s[kKeys / 32];
 #pragma unroll
     for (int f = 0; f < kKeys / 32; ++f) {
@@ -137,17 +154,41 @@ __global__ __launch_bounds__(kFWaves* kWave, 2) void expanded_kernel(const Expan
       for (int d = 0; d < D / 32; ++d) o[d] = mfma(tr_frag<2 * D>(cur->v, vb, 16 * ks, d), p, o[d]);
     }
   };
-  if (n_tiles > 0) copy_kv<D>(a, &tile0, tk0, min(kKeys, nk), h, wave, lane);
-  for (int t = 0; t < n_tiles; t += 2) {   // two tiles a turn: the buffers' addresses are constants
+  copy(&tiles[part][0], part);
+  for (int t = 0; t < n_tiles; t += 2 * PARTS) {   // two tiles a turn: the buffers' addresses are constants
     copies_done_barrier();
-    step(&tile0, &tile1, t);
-    if (t + 1 < n_tiles) {
+    step(&tiles[part][0], &tiles[part][1], t + part);
+    if (t + PARTS < n_tiles) {
       copies_done_barrier();
-      step(&tile1, &tile0, t + 1);
+      step(&tiles[part][1], &tiles[part][0], t + PARTS + part);
+    }
+  }
+  l = half_sum(l);
+  if constexpr (PARTS == 2) {
+    copies_done_barrier();
+    f4* x = reinterpret_cast<f4*>(tiles) + wave * (D / 8) * kWave + lane;   // [wave][register / 4][lane]
+    float* ml = reinterpret_cast<float*>(reinterpret_cast<f4*>(tiles) + kFWaves * (D / 8) * kWave) + wave * 2 * kWave + lane;
+    if (part == 1) {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+        x[i * kWave] = f4{o[i / 4][4 * (i % 4)], o[i / 4][4 * (i % 4) + 1], o[i / 4][4 * (i % 4) + 2], o[i / 4][4 * (i % 4) + 3]};
+      ml[0] = m;
+      ml[kWave] = l;
+    }
+    copies_done_barrier();
+    if (part == 1) return;
+    const float m1 = ml[0], top = fmaxf(m, m1), base = top == kNegInf ? 0.0f : top;
+    const float f0 = __builtin_amdgcn_exp2f(m - base), f1 = __builtin_amdgcn_exp2f(m1 - base);
+    m = top;
+    l = l * f0 + ml[kWave] * f1;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      const f4 v = x[i * kWave];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i / 4][4 * (i % 4) + e] = o[i / 4][4 * (i % 4) + e] * f0 + v[e] * f1;
     }
   }
   if (!live) return;
-  l = half_sum(l);
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
   const int64_t at = ((tq0 + row) * a.H + h) * D + 4 * hh;
 #pragma unroll
@@ -157,6 +198,19 @@ __global__ __launch_bounds__(kFWaves* kWave, 2) void expanded_kernel(const Expan
       store4(a.out, at + 32 * d + 8 * i, a.out_bf16, o[d][4 * i] * inv, o[d][4 * i + 1] * inv,
              o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv);
   if (hh == 0) a.lse[(int64_t)h * a.Tq + tq0 + row] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : kNegInf;
+}
+
+// A CU holds two workgroups of one part or one of two. With fewer than kFewItems (head,
+// tile) pairs the two parts win.
+constexpr int64_t kFewItems = 1024;
+
+template <int D>
+void launch_expanded(const ExpandedArgs& a, hipStream_t s) {
+  const int64_t items = a.slots * a.H;
+  if (items < kFewItems)
+    hipLaunchKernelGGL((expanded_kernel<D, 2>), dim3((unsigned)items), dim3(2 * kFWaves * kWave), 0, s, a);
+  else
+    hipLaunchKernelGGL((expanded_kernel<D, 1>), dim3((unsigned)(a.per_xcd * 8)), dim3(kFWaves * kWave), 0, s, a);
 }
 
 }  // namespace
@@ -181,8 +235,7 @@ extern "C" moe_status moe_latent_attn_expanded(const moe_latent_config* cfg, int
   if (per_xcd * 8 > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
   const ExpandedArgs a{q, kv, k_rope, cu_q, cu_k, out, lse, Tq, Tk, slots, per_xcd, (int)B, cfg->n_heads,
                        scale * kLog2e, causal != 0, ot == MOE_BF16};
-  const dim3 grid((unsigned)(per_xcd * 8)), block(kFWaves * kWave);
-  if (cfg->nope == 128) hipLaunchKernelGGL(expanded_kernel<128>, grid, block, 0, as_stream(stream), a);
-  else hipLaunchKernelGGL(expanded_kernel<64>, grid, block, 0, as_stream(stream), a);
+  if (cfg->nope == 128) launch_expanded<128>(a, as_stream(stream));
+  else launch_expanded<64>(a, as_stream(stream));
   return launch_status();
 }
