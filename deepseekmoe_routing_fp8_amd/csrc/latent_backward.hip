@@ -3,12 +3,24 @@
 // With P = exp(s - lse) recomputed tile by tile and D = rowsum(dO * O):
 //   dV = P^T dO,  dS = P * (dO V^T - D),  dK = scale dS^T Q,  dQ = scale dS K.
 // Two kernels, one per side of the score matrix, so that every sum stays in the registers
-// of one wave in a fixed order (no atomics): the first owns 32 keys a wave and walks the
-// queries (dK, dV), the second owns 32 queries a wave and walks the keys (dQ). Scores are
+// of one wave in a fixed order (no atomics): the first owns 32 queries a wave and walks the
+// keys (dQ), the second owns 32 keys a wave and walks the queries (dK, dV). Scores are
 // formed twice; the alternative, keeping dS, would move H * Tq * Tk values through memory.
+//
+// D from the bf16 output is off by its rounding, and where a softmax is peaked dO V^T - D
+// cancels, so that this error would be the largest of all. A row of dS sums to zero, so the
+// first kernel's row sums are that error: it adds them to D for the second kernel, and takes
+// sum(dS) * P K off its own dQ, for which it also sums P K.
+//
 // The rotary key is shared by the heads: each head's part of its gradient goes to a
 // workspace and a last kernel sums the heads in order. P and dS are rounded to bf16 for
-// the matrix instructions, as the inputs are; everything else is FP32.
+// the matrix instructions, as the inputs are (relative 2^-8 a term, the rounding of the
+// gradients themselves); everything else is FP32.
+//
+// A wave holds its operands and sums in about 400 registers, one wave a SIMD, so the wave
+// itself has to keep both pipes busy: the scores of the next 32 rows are formed while the
+// exponentials of the current ones are taken. Tiles come through a ring of three, copied
+// two ahead.
 #include "latent.h"
 
 namespace moe {
@@ -21,10 +33,12 @@ constexpr int kBTile = 64;             // queries (or keys) a step
 struct BackwardArgs {
   const uint16_t *q, *kv, *kr, *dout;
   const int32_t *cu_q, *cu_k;
-  const float *lse, *delta;   // [H, Tq]
+  const uint16_t* out;
+  const float* lse;           // [H, Tq]
+  float *lse2, *delta;        // [H, Tq]: lse in log2 (+inf for a row that sees nothing), D
   void *dq, *dkv;
   float* dkr_part;            // [H, Tk, rope]
-  int64_t Tq, Tk;
+  int64_t Tq, Tk, q_slots, q_per_xcd, k_slots, k_per_xcd;
   int B, H;
   float scale, scale2;        // scale2 = scale * log2(e)
   int causal, bf16;
@@ -43,29 +57,23 @@ __device__ __forceinline__ Span span_of(const BackwardArgs& a, int b) {
   return s;
 }
 
-// delta[h][t] = sum over the value width of dout * out; 16 lanes a (token, head) row.
-template <int D>
-__global__ __launch_bounds__(256) void delta_kernel(const uint16_t* __restrict__ out,
-                                                    const uint16_t* __restrict__ dout, int64_t T, int H,
-                                                    float* __restrict__ delta) {
-  const int64_t r = ((int64_t)blockIdx.x * 256 + threadIdx.x) / 16;
-  const int sub = threadIdx.x & 15;
-  float sum = 0.0f;
-  if (r < T * H) {
-    constexpr int kPer = D / 16;
-    const uint16_t *a = out + r * D + sub * kPer, *b = dout + r * D + sub * kPer;
+// Scheduling of a region of N products, one LDS read each, and the arithmetic beside them:
+// a few reads first, then a product, a read and VALU instructions of the arithmetic in turn.
+template <int N, int VALU>
+__device__ __forceinline__ void spread() {
+  __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 4, 0);
 #pragma unroll
-    for (int i = 0; i < kPer; i += 4) {
-      const uint2 x = *reinterpret_cast<const uint2*>(a + i), y = *reinterpret_cast<const uint2*>(b + i);
-      sum = fmaf(__uint_as_float(x.x << 16), __uint_as_float(y.x << 16), sum);
-      sum = fmaf(__uint_as_float(x.x & 0xffff0000u), __uint_as_float(y.x & 0xffff0000u), sum);
-      sum = fmaf(__uint_as_float(x.y << 16), __uint_as_float(y.y << 16), sum);
-      sum = fmaf(__uint_as_float(x.y & 0xffff0000u), __uint_as_float(y.y & 0xffff0000u), sum);
-    }
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(kSchedValu, VALU, 0);
   }
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor(sum, o, 16);
-  if (r < T * H && sub == 0) delta[(r % H) * T + r / H] = sum;
+}
+
+// Workgroups go to the 8 XCDs in turn: each takes a contiguous part of the (head, tile)
+// list, so that a head's tiles are read through one L2.
+__device__ __forceinline__ int64_t list_item(int64_t per_xcd) {
+  return (int64_t)(blockIdx.x & 7) * per_xcd + (blockIdx.x >> 3);
 }
 
 // ---------------------------------------------------------------------------------
@@ -74,7 +82,7 @@ __global__ __launch_bounds__(256) void delta_kernel(const uint16_t* __restrict__
 template <int D>
 struct __attribute__((aligned(256))) QTile {
   uint8_t q[kBTile * 2 * D], r[kBTile * 2 * kRope], g[kBTile * 2 * D];   // q (nope, rope), dout
-  float lse[kBTile], delta[kBTile];
+  float lse2[kBTile], delta[kBTile];
 };
 
 template <int D>
@@ -87,20 +95,22 @@ __device__ __forceinline__ void copy_q(const BackwardArgs& a, QTile<D>* t, int64
   tile_copy<2 * kRope, kBTile, kBWaves>(q, qs, 2 * D, t->r, wave, lane);
   tile_copy<2 * D, kBTile, kBWaves>(g, gs, 0, t->g, wave, lane);
   if (wave < 2) {   // a value a lane
-    const float* src = wave == 0 ? a.lse : a.delta;
+    const float* src = wave == 0 ? a.lse2 : a.delta;
     const auto s = buffer_of(src + (int64_t)h * a.Tq + row0, (int64_t)n * 4);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(s, (lds_byte*)(wave == 0 ? t->lse : t->delta), 4, lane * 4, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(s, (lds_byte*)(wave == 0 ? t->lse2 : t->delta), 4, lane * 4, 0, 0, 0);
   }
 }
 
 template <int D>
 __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_kv_kernel(const BackwardArgs a) {
   constexpr int kSteps = (D + kRope) / 16;
-  __shared__ QTile<D> tiles[2];
+  __shared__ QTile<D> tile0, tile1, tile2;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, hh = lane >> 5;
-  const int h = blockIdx.x % a.H;
-  const SeqTile st = find_seq<kBRows>(a.cu_k, a.B, blockIdx.x / a.H);
+  const int64_t id = list_item(a.k_per_xcd);
+  if (id >= a.k_slots * a.H) return;
+  const int h = (int)(id / a.k_slots);
+  const SeqTile st = find_seq<kBRows>(a.cu_k, a.B, id % a.k_slots);
   const Span sp = span_of(a, st.b);
   if (st.tile < 0 || (int64_t)st.tile * kBRows >= sp.nk) return;
   const int w0 = st.tile * kBRows + wave * 32;   // the wave's first key
@@ -128,51 +138,86 @@ __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_kv_kernel(const Ba
   const int qb = row_base<2 * D>(lane), rb = row_base<2 * kRope>(lane);
   const int qt = tr_base<2 * D>(lane), rt = tr_base<2 * kRope>(lane);
 
-  // queries from the first that sees this workgroup's first key
+  // queries from the first that sees this workgroup's first key, 64 a tile
   const int first = a.causal ? max(0, st.tile * kBRows - ahead) / kBTile * kBTile : 0;
-  if (first < sp.nq) copy_q<D>(a, &tiles[0], sp.q0 + first, min(kBTile, sp.nq - first), h, wave, lane);
-  for (int t0 = first, it = 0; t0 < sp.nq; t0 += kBTile, ++it) {
-    copies_done_barrier();
-    if (t0 + kBTile < sp.nq)
-      copy_q<D>(a, &tiles[(it + 1) & 1], sp.q0 + t0 + kBTile, min(kBTile, sp.nq - t0 - kBTile), h, wave, lane);
-    const QTile<D>& tl = tiles[it & 1];
-    const bool edge = a.causal && t0 + ahead < w0 + 31;   // some query hides some key
+  const int n_tiles = max(0, (sp.nq - first + kBTile - 1) / kBTile);
+  auto copy = [&](QTile<D>& to, int t) __attribute__((always_inline)) {
+    const int t0 = first + t * kBTile;
+    if (t < n_tiles) copy_q<D>(a, &to, sp.q0 + t0, min(kBTile, sp.nq - t0), h, wave, lane);
+  };
+  // S = Q K^T and dP = dO V^T for 32 queries of a tile
+  auto scores = [&](const QTile<D>& tl, int f, f16v& s, f16v& dp) __attribute__((always_inline)) {
+    s = zero16();
+    dp = zero16();
 #pragma unroll
-    for (int f = 0; f < kBTile / 32; ++f) {
-      f16v s = zero16(), dp = zero16();
+    for (int i = 0; i < D / 16; ++i) {
+      s = mfma(row_frag<2 * D>(tl.q, qb, 32 * f, i), kf[i], s);
+      dp = mfma(row_frag<2 * D>(tl.g, qb, 32 * f, i), vf[i], dp);
+    }
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) s = mfma(row_frag<2 * D>(tl.q, qb, 32 * f, i), kf[i], s);
+    for (int i = 0; i < kRope / 16; ++i) s = mfma(row_frag<2 * kRope>(tl.r, rb, 32 * f, i), kf[D / 16 + i], s);
+  };
+  // P in place of S, dS in place of dP. Queries past the end were read as zeros (lse, D,
+  // q and dout): P = 1 there, but dout and dS are 0, so they add nothing.
+  auto weights = [&](const QTile<D>& tl, int f, f16v& s, f16v& dp) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < kRope / 16; ++i) s = mfma(row_frag<2 * kRope>(tl.r, rb, 32 * f, i), kf[D / 16 + i], s);
+    for (int i = 0; i < 4; ++i) {
+      const f4 ls = *reinterpret_cast<const f4*>(tl.lse2 + 32 * f + 8 * i + 4 * hh);
+      const f4 de = *reinterpret_cast<const f4*>(tl.delta + 32 * f + 8 * i + 4 * hh);
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) dp = mfma(row_frag<2 * D>(tl.g, qb, 32 * f, i), vf[i], dp);
-      // queries past the end were read as zeros: lse 0, score 0, dout 0, so they add nothing
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f4 ls = *reinterpret_cast<const f4*>(tl.lse + 32 * f + 8 * i + 4 * hh);
-        const f4 de = *reinterpret_cast<const f4*>(tl.delta + 32 * f + 8 * i + 4 * hh);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = 4 * i + e;
-          float p = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale2, -ls[e] * kLog2e));
-          if (edge && key > t0 + 32 * f + 8 * i + 4 * hh + e + ahead) p = 0.0f;
-          s[r] = p;
-          dp[r] = p * (dp[r] - de[e]);
-        }
-      }
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        const bf8 p = b_operand(s, ks), ds = b_operand(dp, ks);
-        const int r0 = 32 * f + 16 * ks;
-#pragma unroll
-        for (int d = 0; d < D / 32; ++d) {
-          dv[d] = mfma(tr_frag<2 * D>(tl.g, qt, r0, d), p, dv[d]);
-          dk[d] = mfma(tr_frag<2 * D>(tl.q, qt, r0, d), ds, dk[d]);
-        }
-#pragma unroll
-        for (int d = 0; d < kRope / 32; ++d) dr[d] = mfma(tr_frag<2 * kRope>(tl.r, rt, r0, d), ds, dr[d]);
+      for (int e = 0; e < 4; ++e) {
+        const float p = __builtin_amdgcn_exp2f(fmaf(s[4 * i + e], a.scale2, -ls[e]));
+        s[4 * i + e] = p;
+        dp[4 * i + e] = p * (dp[4 * i + e] - de[e]);
       }
     }
+  };
+  auto hide = [&](int t, int f, f16v& s, f16v& dp) __attribute__((always_inline)) {
+    const int q0 = first + t * kBTile + 32 * f + ahead;   // the last key that the first query sees
+    if (a.causal && q0 < w0 + 31) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (key > q0 + 8 * (r / 4) + 4 * hh + r % 4) s[r] = dp[r] = 0.0f;
+    }
+  };
+  auto sums = [&](const QTile<D>& tl, int f, const f16v& s, const f16v& dp) __attribute__((always_inline)) {
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      const bf8 p = b_operand(s, ks), ds = b_operand(dp, ks);
+      const int r0 = 32 * f + 16 * ks;
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d) {
+        dv[d] = mfma(tr_frag<2 * D>(tl.g, qt, r0, d), p, dv[d]);
+        dk[d] = mfma(tr_frag<2 * D>(tl.q, qt, r0, d), ds, dk[d]);
+      }
+#pragma unroll
+      for (int d = 0; d < kRope / 32; ++d) dr[d] = mfma(tr_frag<2 * kRope>(tl.r, rt, r0, d), ds, dr[d]);
+    }
+  };
+  f16v s0, d0, s1, d1;
+  // One tile: its first 32 queries' scores are there on entry; the next tile's are on exit.
+  auto turn = [&](const QTile<D>& cur, const QTile<D>& next, QTile<D>& far, int t) __attribute__((always_inline)) {
+    scores(cur, 1, s1, d1);
+    weights(cur, 0, s0, d0);
+    spread<D / 16 * 2 + kRope / 16, 8>();
+    hide(t, 0, s0, d0);
+    sums(cur, 0, s0, d0);
+    copies_done_barrier();   // the next tile has arrived, and every wave is done with the last
+    copy(far, t + 2);
+    scores(next, 0, s0, d0);   // (of nothing after the last tile: not used)
+    weights(cur, 1, s1, d1);
+    spread<D / 16 * 2 + kRope / 16, 8>();
+    hide(t, 1, s1, d1);
+    sums(cur, 1, s1, d1);
+  };
+  copy(tile0, 0);
+  copies_done_barrier();
+  copy(tile1, 1);
+  if (n_tiles > 0) scores(tile0, 0, s0, d0);
+  for (int t = 0; t < n_tiles; t += 3) {
+    turn(tile0, tile1, tile2, t);
+    if (t + 1 < n_tiles) turn(tile1, tile2, tile0, t + 1);
+    if (t + 2 < n_tiles) turn(tile2, tile0, tile1, t + 2);
   }
   if (key >= sp.nk) return;
   const int64_t at = ((sp.k0 + key) * a.H + h) * 2 * D + 4 * hh;
@@ -226,96 +271,146 @@ __device__ __forceinline__ void copy_k(const BackwardArgs& a, KTile<D>* t, int64
 
 template <int D>
 __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_q_kernel(const BackwardArgs a) {
-  constexpr int kSteps = (D + kRope) / 16;
-  __shared__ KTile<D> tiles[2];
+  constexpr int kSteps = (D + kRope) / 16, kBlocks = (D + kRope) / 32;
+  __shared__ KTile<D> tile0, tile1, tile2;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, hh = lane >> 5;
-  const int h = blockIdx.x % a.H;
-  const SeqTile st = find_seq<kBRows>(a.cu_q, a.B, blockIdx.x / a.H);
+  const int64_t id = list_item(a.q_per_xcd);
+  if (id >= a.q_slots * a.H) return;
+  const int h = (int)(id / a.q_slots);
+  const SeqTile st = find_seq<kBRows>(a.cu_q, a.B, a.q_slots - 1 - id % a.q_slots);
   const Span sp = span_of(a, st.b);
   if (st.tile < 0 || (int64_t)st.tile * kBRows >= sp.nq) return;
   const int wg0 = st.tile * kBRows, w0 = wg0 + wave * 32, row = w0 + col;
   const int ahead = sp.nk - sp.nq;
-  const int limit = a.causal ? min(sp.nk, row + ahead + 1) : sp.nk;
+  const int limit = a.causal ? min(sp.nk, row + ahead + 1) : sp.nk;   // keys that this lane's query sees
   const int wg_limit = a.causal ? min(sp.nk, min(wg0 + kBRows, sp.nq) + ahead) : sp.nk;
   const int n_tiles = max(0, (wg_limit + kBTile - 1) / kBTile);
 
   bf8 qf[kSteps], gf[D / 16];
-  const int64_t rc = sp.q0 + min(row, sp.nq - 1);
+  const int64_t rc = sp.q0 + min(row, sp.nq - 1), sc = (int64_t)h * a.Tq + rc;
+  float lse2 = a.lse[sc] * kLog2e, delta = 0.0f;
+  if (lse2 == kNegInf) lse2 = -kNegInf;   // a row that sees nothing: every weight 0
   {
     const uint16_t* qp = a.q + (rc * a.H + h) * (D + kRope) + 8 * hh;
     const uint16_t* gp = a.dout + (rc * a.H + h) * D + 8 * hh;
+    const uint16_t* op = a.out + (rc * a.H + h) * D + 8 * hh;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) qf[s] = *reinterpret_cast<const bf8*>(qp + 16 * s);
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s) gf[s] = *reinterpret_cast<const bf8*>(gp + 16 * s);
-  }
-  const float lse2 = a.lse[(int64_t)h * a.Tq + rc] * kLog2e, delta = a.delta[(int64_t)h * a.Tq + rc];
-  f16v dq[D / 32 + kRope / 32];
+    for (int s = 0; s < D / 16; ++s) {
+      gf[s] = *reinterpret_cast<const bf8*>(gp + 16 * s);
+      const bf8 o = *reinterpret_cast<const bf8*>(op + 16 * s);
 #pragma unroll
-  for (int d = 0; d < D / 32 + kRope / 32; ++d) dq[d] = zero16();
+      for (int e = 0; e < 8; ++e) delta = fmaf((float)gf[s][e], (float)o[e], delta);
+    }
+    delta = half_sum(delta);
+  }
+  f16v dq[kBlocks], pk[kBlocks];
+#pragma unroll
+  for (int d = 0; d < kBlocks; ++d) dq[d] = pk[d] = zero16();
+  float off = 0.0f;   // this lane's part of the row sum of dS
   const int kb = row_base<2 * D>(lane), rb = row_base<2 * kRope>(lane);
   const int kt = tr_base<2 * D>(lane), rt = tr_base<2 * kRope>(lane);
 
-  if (n_tiles > 0) copy_k<D>(a, &tiles[0], sp.k0, min(kBTile, sp.nk), h, wave, lane);
-  for (int t = 0; t < n_tiles; ++t) {
-    copies_done_barrier();
-    const int k0 = t * kBTile;
-    if (t + 1 < n_tiles)
-      copy_k<D>(a, &tiles[(t + 1) & 1], sp.k0 + k0 + kBTile, min(kBTile, sp.nk - k0 - kBTile), h, wave, lane);
-    const KTile<D>& tl = tiles[t & 1];
-    const bool edge = k0 + kBTile > (a.causal ? min(sp.nk, w0 + ahead + 1) : sp.nk);
+  auto copy = [&](KTile<D>& to, int t) __attribute__((always_inline)) {
+    if (t < n_tiles) copy_k<D>(a, &to, sp.k0 + t * kBTile, min(kBTile, sp.nk - t * kBTile), h, wave, lane);
+  };
+  // S^T = K Q^T and dP^T = V dO^T for 32 keys of a tile
+  auto scores = [&](const KTile<D>& tl, int f, f16v& s, f16v& dp) __attribute__((always_inline)) {
+    s = zero16();
+    dp = zero16();
 #pragma unroll
-    for (int f = 0; f < kBTile / 32; ++f) {
-      f16v s = zero16(), dp = zero16();
+    for (int i = 0; i < D / 16; ++i) {
+      s = mfma(row_frag<2 * D>(tl.k, kb, 32 * f, i), qf[i], s);
+      dp = mfma(row_frag<2 * D>(tl.v, kb, 32 * f, i), gf[i], dp);
+    }
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) s = mfma(row_frag<2 * D>(tl.k, kb, 32 * f, i), qf[i], s);
+    for (int i = 0; i < kRope / 16; ++i) s = mfma(row_frag<2 * kRope>(tl.r, rb, 32 * f, i), qf[D / 16 + i], s);
+  };
+  auto weights = [&](f16v& s, f16v& dp) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < kRope / 16; ++i) s = mfma(row_frag<2 * kRope>(tl.r, rb, 32 * f, i), qf[D / 16 + i], s);
+    for (int r = 0; r < 16; ++r) {
+      s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale2, -lse2));
+      dp[r] = s[r] * (dp[r] - delta);
+    }
+  };
+  auto hide = [&](int t, int f, f16v& s, f16v& dp) __attribute__((always_inline)) {
+    const int k0 = t * kBTile + 32 * f;
+    if (k0 + 32 > (a.causal ? min(sp.nk, w0 + ahead + 1) : sp.nk)) {
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) dp = mfma(row_frag<2 * D>(tl.v, kb, 32 * f, i), gf[i], dp);
+      for (int r = 0; r < 16; ++r)
+        if (k0 + 8 * (r / 4) + 4 * hh + r % 4 >= limit) s[r] = dp[r] = 0.0f;
+    }
+  };
+  auto sums = [&](const KTile<D>& tl, int f, const f16v& s, const f16v& dp) __attribute__((always_inline)) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        float p = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale2, -lse2));
-        if (edge && k0 + 32 * f + 8 * (r / 4) + 4 * hh + r % 4 >= limit) p = 0.0f;
-        dp[r] = p * (dp[r] - delta);
-      }
+    for (int r = 0; r < 16; ++r) off += dp[r];
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        const bf8 ds = b_operand(dp, ks);
-        const int r0 = 32 * f + 16 * ks;
+    for (int ks = 0; ks < 2; ++ks) {
+      const bf8 p = b_operand(s, ks), ds = b_operand(dp, ks);
+      const int r0 = 32 * f + 16 * ks;
 #pragma unroll
-        for (int d = 0; d < D / 32; ++d) dq[d] = mfma(tr_frag<2 * D>(tl.k, kt, r0, d), ds, dq[d]);
-#pragma unroll
-        for (int d = 0; d < kRope / 32; ++d)
-          dq[D / 32 + d] = mfma(tr_frag<2 * kRope>(tl.r, rt, r0, d), ds, dq[D / 32 + d]);
+      for (int d = 0; d < kBlocks; ++d) {
+        const bf8 k = d < D / 32 ? tr_frag<2 * D>(tl.k, kt, r0, d < D / 32 ? d : 0)
+                                 : tr_frag<2 * kRope>(tl.r, rt, r0, d < D / 32 ? 0 : d - D / 32);
+        dq[d] = mfma(k, ds, dq[d]);
+        pk[d] = mfma(k, p, pk[d]);
       }
     }
+  };
+  f16v s0, d0, s1, d1;
+  // One tile: its first 32 keys' scores are there on entry; the next tile's are on exit.
+  auto turn = [&](const KTile<D>& cur, const KTile<D>& next, KTile<D>& far, int t) __attribute__((always_inline)) {
+    scores(cur, 1, s1, d1);
+    weights(s0, d0);
+    spread<D / 16 * 2 + kRope / 16, 6>();
+    hide(t, 0, s0, d0);
+    sums(cur, 0, s0, d0);
+    copies_done_barrier();   // the next tile has arrived, and every wave is done with the last
+    copy(far, t + 2);
+    scores(next, 0, s0, d0);   // (of nothing after the last tile: not used)
+    weights(s1, d1);
+    spread<D / 16 * 2 + kRope / 16, 6>();
+    hide(t, 1, s1, d1);
+    sums(cur, 1, s1, d1);
+  };
+  copy(tile0, 0);
+  copies_done_barrier();
+  copy(tile1, 1);
+  if (n_tiles > 0) scores(tile0, 0, s0, d0);
+  for (int t = 0; t < n_tiles; t += 3) {
+    turn(tile0, tile1, tile2, t);
+    if (t + 1 < n_tiles) turn(tile1, tile2, tile0, t + 1);
+    if (t + 2 < n_tiles) turn(tile2, tile0, tile1, t + 2);
   }
   if (row >= sp.nq) return;
+  off = half_sum(off);
+  if (hh == 0) {
+    a.lse2[sc] = lse2;
+    a.delta[sc] = delta + off;
+  }
   const int64_t at = ((sp.q0 + row) * a.H + h) * (D + kRope) + 4 * hh;
 #pragma unroll
-  for (int d = 0; d < D / 32 + kRope / 32; ++d)
+  for (int d = 0; d < kBlocks; ++d)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      store4(a.dq, at + 32 * d + 8 * i, a.bf16, dq[d][4 * i] * a.scale, dq[d][4 * i + 1] * a.scale,
-             dq[d][4 * i + 2] * a.scale, dq[d][4 * i + 3] * a.scale);
+    for (int i = 0; i < 4; ++i) {
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = (dq[d][4 * i + e] - off * pk[d][4 * i + e]) * a.scale;
+      store4(a.dq, at + 32 * d + 8 * i, a.bf16, v[0], v[1], v[2], v[3]);
+    }
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 template <int D>
-void launch_backward(BackwardArgs& a, const uint16_t* out, float* delta, void* dk_rope, hipStream_t s) {
-  const int64_t rows = a.Tq * a.H;
-  if (a.Tq > 0) {
-    hipLaunchKernelGGL(delta_kernel<D>, dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, s, out, a.dout, a.Tq, a.H,
-                       delta);
-    hipLaunchKernelGGL(backward_q_kernel<D>, dim3((unsigned)((a.Tq / kBRows + a.B) * a.H)),
-                       dim3(kBWaves * kWave), 0, s, a);
-  }
+void launch_backward(const BackwardArgs& a, void* dk_rope, hipStream_t s) {
+  const dim3 block(kBWaves * kWave);
+  if (a.Tq > 0)
+    hipLaunchKernelGGL(backward_q_kernel<D>, dim3((unsigned)(a.q_per_xcd * 8)), block, 0, s, a);
   if (a.Tk > 0) {
-    hipLaunchKernelGGL(backward_kv_kernel<D>, dim3((unsigned)((a.Tk / kBRows + a.B) * a.H)),
-                       dim3(kBWaves * kWave), 0, s, a);
+    hipLaunchKernelGGL(backward_kv_kernel<D>, dim3((unsigned)(a.k_per_xcd * 8)), block, 0, s, a);
     hipLaunchKernelGGL(rope_sum_kernel, dim3((unsigned)((a.Tk * kRope / 4 + 255) / 256)), dim3(256), 0, s,
                        a.dkr_part, a.cu_k, a.B, a.Tk, a.H, a.scale, dk_rope, a.bf16);
   }
@@ -329,7 +424,7 @@ using namespace moe;
 extern "C" size_t moe_latent_attn_expanded_backward_workspace_bytes(const moe_latent_config* cfg, int64_t Tq,
                                                                     int64_t Tk) {
   if (check_latent(cfg) != MOE_OK || Tq < 0 || Tk < 0 || Tq > 0x7fffffff || Tk > 0x7fffffff) return 0;
-  return align256((size_t)Tq * cfg->n_heads * 4) + (size_t)Tk * cfg->n_heads * kRope * 4;
+  return 2 * align256((size_t)Tq * cfg->n_heads * 4) + (size_t)Tk * cfg->n_heads * kRope * 4;
 }
 
 extern "C" moe_status moe_latent_attn_expanded_backward(
@@ -350,14 +445,16 @@ extern "C" moe_status moe_latent_attn_expanded_backward(
   for (const void* p : vecs)
     if (misaligned16(p)) return MOE_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < moe_latent_attn_expanded_backward_workspace_bytes(cfg, Tq, Tk)) return MOE_ERR_WORKSPACE;
-  if ((Tq / kBRows + B) * cfg->n_heads > 0x7fffffff || (Tk / kBRows + B) * cfg->n_heads > 0x7fffffff)
-    return MOE_ERR_UNSUPPORTED;
-  if (Tq * cfg->n_heads > (int64_t)1 << 34) return MOE_ERR_UNSUPPORTED;
-  float* delta = static_cast<float*>(ws);
-  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align256((size_t)Tq * cfg->n_heads * 4));
-  BackwardArgs a{q, kv, k_rope, dout, cu_q, cu_k, lse, delta, dq, dkv, part, Tq, Tk, (int)B, cfg->n_heads,
-                 scale, scale * kLog2e, causal != 0, gt == MOE_BF16};
-  if (cfg->nope == 128) launch_backward<128>(a, out, delta, dk_rope, as_stream(stream));
-  else launch_backward<64>(a, out, delta, dk_rope, as_stream(stream));
+  const int64_t q_slots = Tq / kBRows + B, k_slots = Tk / kBRows + B;
+  const int64_t q_per_xcd = (q_slots * cfg->n_heads + 7) / 8, k_per_xcd = (k_slots * cfg->n_heads + 7) / 8;
+  if (q_per_xcd * 8 > 0x7fffffff || k_per_xcd * 8 > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  const size_t row_bytes = align256((size_t)Tq * cfg->n_heads * 4);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  const BackwardArgs a{q, kv, k_rope, dout, cu_q, cu_k, out, lse, reinterpret_cast<float*>(w),
+                       reinterpret_cast<float*>(w + row_bytes), dq, dkv, reinterpret_cast<float*>(w + 2 * row_bytes),
+                       Tq, Tk, q_slots, q_per_xcd, k_slots, k_per_xcd, (int)B, cfg->n_heads, scale, scale * kLog2e,
+                       causal != 0, gt == MOE_BF16};
+  if (cfg->nope == 128) launch_backward<128>(a, dk_rope, as_stream(stream));
+  else launch_backward<64>(a, dk_rope, as_stream(stream));
   return launch_status();
 }

@@ -288,7 +288,8 @@ EXPANDED = [(1, 128, [1], [1], True), (3, 128, [64], [64], True), (2, 128, [65, 
             (2, 128, [40, 7], [10, 0], True), (2, 128, [33, 5], [70, 0], False), (1, 128, [0, 3], [50, 3], True),
             (8, 128, [300], [300], True), (3, 64, [65, 1, 200], [65, 1, 200], True),
             (2, 64, [31, 0, 100], [64, 9, 191], False), (9, 64, [129], [257], True),
-            (1, 128, [700], [700], True), (1, 64, [520], [1100], False)]
+            (1, 128, [700], [700], True), (1, 64, [520], [1100], False),
+            (128, 128, [500, 260], [500, 300], True), (96, 64, [1100, 3], [300, 70], False)]
 
 
 @pytest.mark.parametrize("H,D,nq,nk,causal", EXPANDED)
