@@ -27,8 +27,8 @@ constexpr int kMaxHeads = 1024;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kNegInf = -__builtin_inff();
-// instruction kinds of __builtin_amdgcn_sched_group_barrier
-constexpr int kSchedValu = 0x2, kSchedMfma = 0x8, kSchedLdsRead = 0x100;
+
+
 
 // Host-side validation of a latent-attention configuration.
 inline moe_status check_latent(const moe_latent_config* c) {

@@ -57,18 +57,10 @@ __device__ __forceinline__ Span span_of(const BackwardArgs& a, int b) {
   return s;
 }
 
-// Scheduling of a region of N products, one LDS read each, and the arithmetic beside them:
-// a few reads first, then a product, a read and VALU instructions of the arithmetic in turn.
-template <int N, int VALU>
-__device__ __forceinline__ void spread() {
-  __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 4, 0);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(kSchedLdsRead, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(kSchedValu, VALU, 0);
-  }
-}
+// The products of a tile are laid out by hand, a scheduling barrier after each: LDS reads
+// run kAhead products ahead of the one that takes them (a read takes two to four products'
+// time to arrive), and the arithmetic of the weights is dealt out between the products.
+constexpr int kAhead = 6;
 
 // Workgroups go to the 8 XCDs in turn: each takes a contiguous part of the (head, tile)
 // list, so that a head's tiles are read through one L2.
@@ -145,32 +137,61 @@ __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_kv_kernel(const Ba
     const int t0 = first + t * kBTile;
     if (t < n_tiles) copy_q<D>(a, &to, sp.q0 + t0, min(kBTile, sp.nq - t0), h, wave, lane);
   };
-  // S = Q K^T and dP = dO V^T for 32 queries of a tile
-  auto scores = [&](const QTile<D>& tl, int f, f16v& s, f16v& dp) __attribute__((always_inline)) {
+  // Products of 32 queries of a tile, in order: S = Q K^T and dP = dO V^T by turns, then the
+  // rotary part of S.
+  constexpr int kScores = 2 * (D / 16) + kRope / 16;
+  auto score_row = [&](const QTile<D>& tl, int f, int i) __attribute__((always_inline)) {
+    if (i >= 2 * (D / 16)) return row_frag<2 * kRope>(tl.r, rb, 32 * f, i - 2 * (D / 16));
+    return row_frag<2 * D>(i % 2 == 0 ? tl.q : tl.g, qb, 32 * f, i / 2);
+  };
+  // dV += P^T dO and dK += dS^T Q: (16 queries, product) pairs; product d < D / 32 of dV, of
+  // dK, then of the rotary part
+  constexpr int kPerStep = 2 * (D / 32) + kRope / 32, kSums = 2 * kPerStep;
+  auto sum_col = [&](const QTile<D>& tl, int f, int i) __attribute__((always_inline)) {
+    const int r0 = 32 * f + 16 * (i / kPerStep), d = i % kPerStep;
+    if (d >= 2 * (D / 32)) return tr_frag<2 * kRope>(tl.r, rt, r0, d - 2 * (D / 32));
+    return tr_frag<2 * D>(d % 2 == 0 ? tl.g : tl.q, qt, r0, d / 2);
+  };
+  bf8 rows[kAhead], cols[kAhead];
+  auto ahead_rows = [&](const QTile<D>& tl, int f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) rows[i] = score_row(tl, f, i);
+  };
+  // The scores (s, dp) of (tl, f), whose first rows are there; beside them the weights of
+  // (cur, fc): P in place of sc, dS in place of dc. Queries past the end were read as zeros
+  // (lse, D, q and dout): P = 1 there, but dout and dS are 0, so they add nothing. The first
+  // columns of cur are read at the end.
+  auto scores = [&](const QTile<D>& tl, int f, f16v& s, f16v& dp, const QTile<D>& cur, int fc, f16v& sc, f16v& dc,
+                    bool first_one) __attribute__((always_inline)) {
+    f4 ls = {}, de = {};
+    if (!first_one) {
+      ls = *reinterpret_cast<const f4*>(cur.lse2 + 32 * fc + 4 * hh);
+      de = *reinterpret_cast<const f4*>(cur.delta + 32 * fc + 4 * hh);
+    }
     s = zero16();
     dp = zero16();
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      s = mfma(row_frag<2 * D>(tl.q, qb, 32 * f, i), kf[i], s);
-      dp = mfma(row_frag<2 * D>(tl.g, qb, 32 * f, i), vf[i], dp);
-    }
+    for (int i = 0; i < kScores; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      const int n = i / 2;
+      if (i >= 2 * (D / 16)) s = mfma(rows[i % kAhead], kf[D / 16 + i - 2 * (D / 16)], s);
+      else if (i % 2 == 0) s = mfma(rows[i % kAhead], kf[n], s);
+      else dp = mfma(rows[i % kAhead], vf[n], dp);
+      if (i + kAhead < kScores) rows[i % kAhead] = score_row(tl, f, i + kAhead);
+      if (first_one) continue;
+      if (i >= kScores - kAhead) cols[i - (kScores - kAhead)] = sum_col(cur, fc, i - (kScores - kAhead));
 #pragma unroll
-    for (int i = 0; i < kRope / 16; ++i) s = mfma(row_frag<2 * kRope>(tl.r, rb, 32 * f, i), kf[D / 16 + i], s);
-  };
-  // P in place of S, dS in place of dP. Queries past the end were read as zeros (lse, D,
-  // q and dout): P = 1 there, but dout and dS are 0, so they add nothing.
-  auto weights = [&](const QTile<D>& tl, int f, f16v& s, f16v& dp) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const f4 ls = *reinterpret_cast<const f4*>(tl.lse2 + 32 * f + 8 * i + 4 * hh);
-      const f4 de = *reinterpret_cast<const f4*>(tl.delta + 32 * f + 8 * i + 4 * hh);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float p = __builtin_amdgcn_exp2f(fmaf(s[4 * i + e], a.scale2, -ls[e]));
-        s[4 * i + e] = p;
-        dp[4 * i + e] = p * (dp[4 * i + e] - de[e]);
+      for (int r = i * 16 / kScores; r < (i + 1) * 16 / kScores; ++r) {
+        const float p = __builtin_amdgcn_exp2f(fmaf(sc[r], a.scale2, -ls[r % 4]));
+        sc[r] = p;
+        dc[r] = p * (dc[r] - de[r % 4]);
+        if (r % 4 == 3 && r < 15) {
+          ls = *reinterpret_cast<const f4*>(cur.lse2 + 32 * fc + 8 * (r / 4 + 1) + 4 * hh);
+          de = *reinterpret_cast<const f4*>(cur.delta + 32 * fc + 8 * (r / 4 + 1) + 4 * hh);
+        }
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
   auto hide = [&](int t, int f, f16v& s, f16v& dp) __attribute__((always_inline)) {
     const int q0 = first + t * kBTile + 32 * f + ahead;   // the last key that the first query sees
@@ -180,40 +201,47 @@ __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_kv_kernel(const Ba
         if (key > q0 + 8 * (r / 4) + 4 * hh + r % 4) s[r] = dp[r] = 0.0f;
     }
   };
-  auto sums = [&](const QTile<D>& tl, int f, const f16v& s, const f16v& dp) __attribute__((always_inline)) {
+  // The sums of (tl, f), whose first columns are there; the first rows of (next, fn) are
+  // read at the end.
+  auto sums = [&](const QTile<D>& tl, int f, const f16v& s, const f16v& dp, const QTile<D>& next, int fn)
+      __attribute__((always_inline)) {
+    bf8 p = b_operand(s, 0), ds = b_operand(dp, 0), p1, ds1;
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      const bf8 p = b_operand(s, ks), ds = b_operand(dp, ks);
-      const int r0 = 32 * f + 16 * ks;
-#pragma unroll
-      for (int d = 0; d < D / 32; ++d) {
-        dv[d] = mfma(tr_frag<2 * D>(tl.g, qt, r0, d), p, dv[d]);
-        dk[d] = mfma(tr_frag<2 * D>(tl.q, qt, r0, d), ds, dk[d]);
-      }
-#pragma unroll
-      for (int d = 0; d < kRope / 32; ++d) dr[d] = mfma(tr_frag<2 * kRope>(tl.r, rt, r0, d), ds, dr[d]);
+    for (int i = 0; i < kSums; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (i == kPerStep) p = p1, ds = ds1;
+      const int d = i % kPerStep;
+      if (d >= 2 * (D / 32)) dr[d - 2 * (D / 32)] = mfma(cols[i % kAhead], ds, dr[d - 2 * (D / 32)]);
+      else if (d % 2 == 0) dv[d / 2] = mfma(cols[i % kAhead], p, dv[d / 2]);
+      else dk[d / 2] = mfma(cols[i % kAhead], ds, dk[d / 2]);
+      if (i + kAhead < kSums) cols[i % kAhead] = sum_col(tl, f, i + kAhead);
+      else rows[i - (kSums - kAhead)] = score_row(next, fn, i - (kSums - kAhead));
+      if (i == 1) p1 = b_operand(s, 1);
+      if (i == 2) ds1 = b_operand(dp, 1);
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
   f16v s0, d0, s1, d1;
-  // One tile: its first 32 queries' scores are there on entry; the next tile's are on exit.
+  // One tile: its first 32 queries' scores and its last ones' first rows are there on entry,
+  // the next tile's on exit (of nothing after the last tile: not used).
   auto turn = [&](const QTile<D>& cur, const QTile<D>& next, QTile<D>& far, int t) __attribute__((always_inline)) {
-    scores(cur, 1, s1, d1);
-    weights(cur, 0, s0, d0);
-    spread<D / 16 * 2 + kRope / 16, 8>();
+    scores(cur, 1, s1, d1, cur, 0, s0, d0, false);
     hide(t, 0, s0, d0);
-    sums(cur, 0, s0, d0);
     copies_done_barrier();   // the next tile has arrived, and every wave is done with the last
     copy(far, t + 2);
-    scores(next, 0, s0, d0);   // (of nothing after the last tile: not used)
-    weights(cur, 1, s1, d1);
-    spread<D / 16 * 2 + kRope / 16, 8>();
+    sums(cur, 0, s0, d0, next, 0);
+    scores(next, 0, s0, d0, cur, 1, s1, d1, false);
     hide(t, 1, s1, d1);
-    sums(cur, 1, s1, d1);
+    sums(cur, 1, s1, d1, next, 1);
   };
   copy(tile0, 0);
   copies_done_barrier();
   copy(tile1, 1);
-  if (n_tiles > 0) scores(tile0, 0, s0, d0);
+  if (n_tiles > 0) {
+    ahead_rows(tile0, 0);
+    scores(tile0, 0, s0, d0, tile0, 0, s0, d0, true);
+    ahead_rows(tile0, 1);
+  }
   for (int t = 0; t < n_tiles; t += 3) {
     turn(tile0, tile1, tile2, t);
     if (t + 1 < n_tiles) turn(tile1, tile2, tile0, t + 1);
@@ -316,24 +344,48 @@ __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_q_kernel(const Bac
   auto copy = [&](KTile<D>& to, int t) __attribute__((always_inline)) {
     if (t < n_tiles) copy_k<D>(a, &to, sp.k0 + t * kBTile, min(kBTile, sp.nk - t * kBTile), h, wave, lane);
   };
-  // S^T = K Q^T and dP^T = V dO^T for 32 keys of a tile
-  auto scores = [&](const KTile<D>& tl, int f, f16v& s, f16v& dp) __attribute__((always_inline)) {
+  // Products of 32 keys of a tile, in order: S^T = K Q^T and dP^T = V dO^T by turns, then
+  // the rotary part of S^T.
+  constexpr int kScores = 2 * (D / 16) + kRope / 16;
+  auto score_row = [&](const KTile<D>& tl, int f, int i) __attribute__((always_inline)) {
+    if (i >= 2 * (D / 16)) return row_frag<2 * kRope>(tl.r, rb, 32 * f, i - 2 * (D / 16));
+    return row_frag<2 * D>(i % 2 == 0 ? tl.k : tl.v, kb, 32 * f, i / 2);
+  };
+  // dQ += K^T dS^T and the sum of K^T P^T: (16 keys, 32 columns) pairs, two products each
+  constexpr int kSums = 2 * kBlocks, kColAhead = 4;
+  auto sum_col = [&](const KTile<D>& tl, int f, int i) __attribute__((always_inline)) {
+    const int r0 = 32 * f + 16 * (i / kBlocks), d = i % kBlocks;
+    if (d >= D / 32) return tr_frag<2 * kRope>(tl.r, rt, r0, d - D / 32);
+    return tr_frag<2 * D>(tl.k, kt, r0, d);
+  };
+  bf8 rows[kAhead], cols[kColAhead];
+  auto ahead_rows = [&](const KTile<D>& tl, int f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) rows[i] = score_row(tl, f, i);
+  };
+  // The scores (s, dp) of (tl, f), whose first rows are there; beside them the weights of
+  // (cur, fc): P in place of sc, dS in place of dc. The first columns of cur are read at the
+  // end.
+  auto scores = [&](const KTile<D>& tl, int f, f16v& s, f16v& dp, const KTile<D>& cur, int fc, f16v& sc, f16v& dc,
+                    bool first_one) __attribute__((always_inline)) {
     s = zero16();
     dp = zero16();
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      s = mfma(row_frag<2 * D>(tl.k, kb, 32 * f, i), qf[i], s);
-      dp = mfma(row_frag<2 * D>(tl.v, kb, 32 * f, i), gf[i], dp);
-    }
+    for (int i = 0; i < kScores; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (i >= 2 * (D / 16)) s = mfma(rows[i % kAhead], qf[D / 16 + i - 2 * (D / 16)], s);
+      else if (i % 2 == 0) s = mfma(rows[i % kAhead], qf[i / 2], s);
+      else dp = mfma(rows[i % kAhead], gf[i / 2], dp);
+      if (i + kAhead < kScores) rows[i % kAhead] = score_row(tl, f, i + kAhead);
+      if (first_one) continue;
+      if (i >= kScores - kColAhead) cols[i - (kScores - kColAhead)] = sum_col(cur, fc, i - (kScores - kColAhead));
 #pragma unroll
-    for (int i = 0; i < kRope / 16; ++i) s = mfma(row_frag<2 * kRope>(tl.r, rb, 32 * f, i), qf[D / 16 + i], s);
-  };
-  auto weights = [&](f16v& s, f16v& dp) __attribute__((always_inline)) {
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      s[r] = __builtin_amdgcn_exp2f(fmaf(s[r], a.scale2, -lse2));
-      dp[r] = s[r] * (dp[r] - delta);
+      for (int r = i * 16 / kScores; r < (i + 1) * 16 / kScores; ++r) {
+        sc[r] = __builtin_amdgcn_exp2f(fmaf(sc[r], a.scale2, -lse2));
+        dc[r] = sc[r] * (dc[r] - delta);
+      }
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
   auto hide = [&](int t, int f, f16v& s, f16v& dp) __attribute__((always_inline)) {
     const int k0 = t * kBTile + 32 * f;
@@ -343,42 +395,48 @@ __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_q_kernel(const Bac
         if (k0 + 8 * (r / 4) + 4 * hh + r % 4 >= limit) s[r] = dp[r] = 0.0f;
     }
   };
-  auto sums = [&](const KTile<D>& tl, int f, const f16v& s, const f16v& dp) __attribute__((always_inline)) {
+  // The sums of (tl, f), whose first columns are there; the first rows of (next, fn) are
+  // read at the end.
+  auto sums = [&](const KTile<D>& tl, int f, const f16v& s, const f16v& dp, const KTile<D>& next, int fn)
+      __attribute__((always_inline)) {
+    bf8 p = b_operand(s, 0), ds = b_operand(dp, 0), p1, ds1;
 #pragma unroll
-    for (int r = 0; r < 16; ++r) off += dp[r];
+    for (int i = 0; i < kSums; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      if (i == kBlocks) p = p1, ds = ds1;
+      const int d = i % kBlocks;
+      dq[d] = mfma(cols[i % kColAhead], ds, dq[d]);
+      pk[d] = mfma(cols[i % kColAhead], p, pk[d]);
+      if (i + kColAhead < kSums) cols[i % kColAhead] = sum_col(tl, f, i + kColAhead);
+      if (i >= kSums - kAhead) rows[i - (kSums - kAhead)] = score_row(next, fn, i - (kSums - kAhead));
+      if (i == 0) p1 = b_operand(s, 1);
+      if (i == 1) ds1 = b_operand(dp, 1);
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      const bf8 p = b_operand(s, ks), ds = b_operand(dp, ks);
-      const int r0 = 32 * f + 16 * ks;
-#pragma unroll
-      for (int d = 0; d < kBlocks; ++d) {
-        const bf8 k = d < D / 32 ? tr_frag<2 * D>(tl.k, kt, r0, d < D / 32 ? d : 0)
-                                 : tr_frag<2 * kRope>(tl.r, rt, r0, d < D / 32 ? 0 : d - D / 32);
-        dq[d] = mfma(k, ds, dq[d]);
-        pk[d] = mfma(k, p, pk[d]);
-      }
+      for (int r = i * 16 / kSums; r < (i + 1) * 16 / kSums; ++r) off += dp[r];
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
   f16v s0, d0, s1, d1;
-  // One tile: its first 32 keys' scores are there on entry; the next tile's are on exit.
+  // One tile: its first 32 keys' scores and its last ones' first rows are there on entry,
+  // the next tile's on exit (of nothing after the last tile: not used).
   auto turn = [&](const KTile<D>& cur, const KTile<D>& next, KTile<D>& far, int t) __attribute__((always_inline)) {
-    scores(cur, 1, s1, d1);
-    weights(s0, d0);
-    spread<D / 16 * 2 + kRope / 16, 6>();
+    scores(cur, 1, s1, d1, cur, 0, s0, d0, false);
     hide(t, 0, s0, d0);
-    sums(cur, 0, s0, d0);
     copies_done_barrier();   // the next tile has arrived, and every wave is done with the last
     copy(far, t + 2);
-    scores(next, 0, s0, d0);   // (of nothing after the last tile: not used)
-    weights(s1, d1);
-    spread<D / 16 * 2 + kRope / 16, 6>();
+    sums(cur, 0, s0, d0, next, 0);
+    scores(next, 0, s0, d0, cur, 1, s1, d1, false);
     hide(t, 1, s1, d1);
-    sums(cur, 1, s1, d1);
+    sums(cur, 1, s1, d1, next, 1);
   };
   copy(tile0, 0);
   copies_done_barrier();
   copy(tile1, 1);
-  if (n_tiles > 0) scores(tile0, 0, s0, d0);
+  if (n_tiles > 0) {
+    ahead_rows(tile0, 0);
+    scores(tile0, 0, s0, d0, tile0, 0, s0, d0, true);
+    ahead_rows(tile0, 1);
+  }
   for (int t = 0; t < n_tiles; t += 3) {
     turn(tile0, tile1, tile2, t);
     if (t + 1 < n_tiles) turn(tile1, tile2, tile0, t + 1);
