@@ -74,6 +74,17 @@ __device__ __forceinline__ float half_sum(float v) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
+// The value of the lane 16 away combined with the own one (v_permlane16_swap exchanges odd
+// rows of 16 lanes of one operand with even rows of the other).
+__device__ __forceinline__ float row_max(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float row_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
 // Registers 8 * ks .. 8 * ks + 7 of a result as the B operand of depth step ks.
 __device__ __forceinline__ bf8 b_operand(const f16v& s, int ks) {
   union { uint32_t u[4]; bf8 v; } r;

@@ -7,14 +7,20 @@
 //
 // A wave owns 16 query rows: their operands (72 registers at latent 512) and their part of
 // O (128) are what two waves a SIMD can hold. The eight waves of a workgroup are WQ groups
-// of query rows x WT tiles worked on side by side x WD parts of the value width (the
-// scores are then formed by each part), by the number of query rows.
+// of query rows x WD parts of the value width (each part forms the scores anew), by the
+// number of query rows.
 //
-// The work is the sequences' steps of 32 WT rows laid end to end, (sequence, block of query
-// rows, step), cut into equal ranges for a fixed number of workgroups: ragged lengths
-// balance without the host knowing them. A block of query rows whose steps fall into
-// several ranges leaves its partial sums (O unnormalised, maximum, sum, all FP32) in the
-// workspace, and a second kernel joins them in range order.
+// The work is the sequences' tiles laid end to end, (sequence, block of query rows, tile),
+// cut into equal ranges for a fixed number of workgroups: ragged lengths balance without
+// the host knowing them. A block of query rows whose tiles fall into several ranges leaves
+// its partial sums (O unnormalised, maximum, sum, all FP32) in the workspace, and a second
+// kernel joins them in range order.
+//
+// Rows come by direct copies to LDS, several tiles ahead: a bf16 tile is worked on as it
+// lands; E4M3 rows land as codes, and the wave that copied them writes them out as bf16 a
+// tile ahead of the products (exact: the scales are powers of two). Every wave issues the
+// same number of copies for every tile, also past the end of its range (rows that are not
+// there, which read as zeros), so that the wait for a tile is a constant.
 #include "latent.h"
 
 namespace moe {
@@ -24,7 +30,7 @@ constexpr int kTok = 32;        // cached rows a tile
 constexpr int kAWaves = 8;
 constexpr int kAThreads = kAWaves * kWave;
 constexpr int kGroups = 256;    // workgroups: one a CU
-constexpr int kMinSteps = 2;    // steps a range holds at least
+constexpr int kMinTiles = 2;    // tiles a range holds at least
 constexpr int kAhead = 3;         // depth steps whose rows are read ahead
 constexpr float kSlack = 8.0f;  // how far (log2) a score may pass the reference of its row
 
@@ -34,7 +40,7 @@ struct AbsorbedArgs {
   const int32_t *table, *lengths;
   void* out;
   float* lse;
-  int64_t* first;      // [B + 1]: steps before each sequence (one block of query rows)
+  int64_t* first;      // [B + 1]: tiles before each sequence (one block of query rows)
   float* part;         // [kGroups][2] partial results
   int64_t n_pages, max_pages;
   int B, Sq, H, page, blocks;   // blocks of query rows a sequence
@@ -49,8 +55,8 @@ __device__ __forceinline__ f4 mfma16(bf8 a, bf8 b, f4 c) {
 __device__ __forceinline__ int length_of(const AbsorbedArgs& a, int b) {
   return (int)min((int64_t)max(a.lengths[b], 0), a.max_pages * a.page);
 }
-__device__ __forceinline__ int64_t range_steps(int64_t total) {
-  return max((int64_t)kMinSteps, (total + kGroups - 1) / kGroups);
+__device__ __forceinline__ int64_t range_tiles(int64_t total) {
+  return max((int64_t)kMinTiles, (total + kGroups - 1) / kGroups);
 }
 // floats of a partial result of n query rows: O, then the maxima and the sums
 __host__ __device__ constexpr int64_t part_floats(int latent, int n) { return (int64_t)n * (latent + 2); }
@@ -72,187 +78,206 @@ struct __attribute__((aligned(256))) LatentTile {
   uint8_t c[kTok * 2 * R], r[kTok * 2 * kRope];
 };
 
-// Cache rows of a step staged by a wave, one row an instruction. A row that is not there
-// (past the length, page out of range) is zero.
-template <int R, int WT, bool FP8>
-struct Stage {
-  static constexpr int kRows = kTok * WT / kAWaves;
-  u4 v[FP8 ? kRows : 1];
-  float s[FP8 ? kRows : 1];
-};
+constexpr int kRows = kTok / kAWaves;      // rows of a tile that a wave copies
+constexpr int kBatch = kWave / kRows;      // tiles whose pages a wave looks up at a time
 
-// The page of position pos of sequence b as the table has it (the table's last column for a
-// position past it); a row number is formed from it a step later, when it has arrived.
-__device__ __forceinline__ int page_of(const AbsorbedArgs& a, int b, int pos) {
-  const int64_t p = min((int64_t)((uint32_t)pos / (uint32_t)a.page), a.max_pages - 1);
-  return a.table[(int64_t)b * a.max_pages + p];
-}
-// The cache row of position pos, -1 if there is none.
-__device__ __forceinline__ int row_slot(const AbsorbedArgs& a, int pg, int pos, int len) {
-  const bool there = pos < len && pg >= 0 && pg < a.n_pages;
-  return there ? pg * a.page + (int)((uint32_t)pos % (uint32_t)a.page) : -1;
-}
-
-// slots: lane j < kRows holds the cache row of the wave's j-th row.
-template <int R, int WT, bool FP8>
-__device__ __forceinline__ void load_rows(const AbsorbedArgs& a, Stage<R, WT, FP8>& g, LatentTile<R>* tiles, int slots,
-                                          int wave, int lane) {
-  constexpr int kRows = Stage<R, WT, FP8>::kRows, kBytes = cache_row_bytes(R, FP8);
-  LatentTile<R>* t = tiles + wave * kRows / kTok;
-  const int row0 = wave * kRows % kTok;
-#pragma unroll
-  for (int j = 0; j < kRows; ++j) {
-    const int slot = __builtin_amdgcn_readlane(slots, j);
-    const auto row = buffer_of(a.cache + (int64_t)max(slot, 0) * kBytes, slot >= 0 ? kBytes : 0);
-    if constexpr (FP8) {
-      // lanes of 16 codes, then 8 lanes of the rotary key; the lane's scale beside them
-      g.v[j] = __builtin_bit_cast(u4, __builtin_amdgcn_raw_buffer_load_b128(row, lane * 16, 0, 0));
-      g.s[j] = __builtin_bit_cast(
-          float, __builtin_amdgcn_raw_buffer_load_b32(row, R + 2 * kRope + 4 * min(lane / 8, R / kTile - 1), 0, 0));
-    } else {
-      const int r = row0 + j;
-      if (lane < R / 8) {
-        const int c = (lane & ~15) | ((lane ^ latent_key(r)) & 15);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(row, (lds_byte*)(t->c + r * 2 * R), 16, c * 16, 0, 0, 0);
-      }
-    }
-  }
-  if constexpr (!FP8) {
-    // rotary keys: lane l stages the 16 bytes at l * 16 of the wave's 128-byte rows
-    if (lane < kRows * 8) {
-      const int line = row0 / 2 + (lane >> 4);
-      const int x = (lane & 15) ^ line_key(line);
-      const int slot = __shfl(slots, 2 * line + (x >> 3) - row0);
-      uint8_t* to = t->r + row0 * 128;
-      if (slot >= 0)
-        __builtin_amdgcn_global_load_lds(a.cache + (int64_t)slot * kBytes + 2 * R + (x & 7) * 16, (lds_byte*)to, 16, 0, 0);
-      else
-        *reinterpret_cast<u4*>(to + lane * 16) = u4{0, 0, 0, 0};
-    }
-  }
-}
-
-template <int R, int WT>
-__device__ __forceinline__ void store_rows(const Stage<R, WT, true>& g, LatentTile<R>* tiles, int wave, int lane) {
-  constexpr int kRows = Stage<R, WT, true>::kRows;
-  LatentTile<R>* t = tiles + wave * kRows / kTok;
-#pragma unroll
-  for (int j = 0; j < kRows; ++j) {
-    const int r = wave * kRows % kTok + j;
-    if (lane < R / 16) {
-      *reinterpret_cast<u4*>(t->c + latent_off<R>(r, 2 * lane)) = unpack_fp8(make_uint2(g.v[j][0], g.v[j][1]), g.s[j]);
-      *reinterpret_cast<u4*>(t->c + latent_off<R>(r, 2 * lane + 1)) = unpack_fp8(make_uint2(g.v[j][2], g.v[j][3]), g.s[j]);
-    } else if (lane < R / 16 + 8) {
-      *reinterpret_cast<u4*>(t->r + tile_off<2 * kRope>(r, lane - R / 16)) = g.v[j];
-    }
-  }
-}
-
-// E4M3 rows by way of LDS (one tile a step): a wave copies its rows' codes there one step
-// ahead of the conversion, so no register waits on memory across the products.
 template <int R>
 struct __attribute__((aligned(16))) CodeTile {
   uint8_t row[kTok][fp8_row_bytes(R)];
 };
 
+// Buffers of a workgroup. bf16: NT tiles, the copies NT - 1 ahead. E4M3: two tiles, and the
+// codes of NC tiles, copied NC ahead of their conversion. QL steps of the query operands
+// wait in LDS where the registers do not hold all of them (128 query rows, latent 512).
+template <int R, int WQ, bool FP8>
+struct Lds {
+  static constexpr int QL = WQ == 8 && R == 512 ? (FP8 ? 8 : 10) : 0;
+  static constexpr int NT = FP8 || QL > 0 ? 2 : 4;
+  static constexpr int NC = FP8 ? (QL > 0 ? 1 : 3) : 0;
+  static constexpr int kAhead = FP8 ? NC + 1 : NT - 1;   // tiles between a copy and its products
+  static constexpr int kCopies = FP8 ? kRows : 2 * kRows;   // a wave's copies for a tile
+  LatentTile<R> tile[NT];
+  CodeTile<FP8 ? R : 16> code[FP8 ? NC : 1];
+  bf8 q[kAWaves][QL > 0 ? QL : 1][kWave];
+  int wsum[kAWaves], found[2];   // find_range
+};
+
+// s_waitcnt: at most n vector-memory operations outstanding, all LDS operations done
+constexpr int wait_vm_lgkm0(int n) { return (n & 0xF) | ((n >> 4) << 14) | 0x0070; }
+
+// Copies the wave's rows of a tile: row j is cache row `slots` of lane l0 + j, or zeros where
+// that is negative (past the length, page out of range).
 template <int R>
-__device__ __forceinline__ void copy_codes(const AbsorbedArgs& a, CodeTile<R>* t, int slots, int wave, int lane) {
-  constexpr int kRows = kTok / kAWaves, kBytes = fp8_row_bytes(R);
+__device__ __forceinline__ void copy_rows(const AbsorbedArgs& a, LatentTile<R>* t, int slots, int l0, int wave,
+                                          int lane) {
+  constexpr int kBytes = cache_row_bytes(R, false);
 #pragma unroll
   for (int j = 0; j < kRows; ++j) {
-    const int slot = __builtin_amdgcn_readlane(slots, j);
+    const int slot = __builtin_amdgcn_readlane(slots, l0 + j);
+    const auto row = buffer_of(a.cache + (int64_t)max(slot, 0) * kBytes, slot >= 0 ? kBytes : 0);
+    const int r = wave * kRows + j;
+    if (lane < R / 8) {
+      const int c = (lane & ~15) | ((lane ^ latent_key(r)) & 15);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(row, (lds_byte*)(t->c + r * 2 * R), 16, c * 16, 0, 0, 0);
+    }
+    // the rotary key is one half of a 256-byte line: lanes of the other half are idle
+    const int x = (lane & 15) ^ line_key(r >> 1);
+    if (lane < 16 && (x >> 3) == (r & 1))
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(row, (lds_byte*)(t->r + (r >> 1) * 256), 16, 2 * R + (x & 7) * 16, 0, 0,
+                                               0);
+  }
+}
+
+template <int R>
+__device__ __forceinline__ void copy_codes(const AbsorbedArgs& a, CodeTile<R>* t, int slots, int l0, int wave,
+                                           int lane) {
+  constexpr int kBytes = fp8_row_bytes(R);
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    const int slot = __builtin_amdgcn_readlane(slots, l0 + j);
     const auto row = buffer_of(a.cache + (int64_t)max(slot, 0) * kBytes, slot >= 0 ? kBytes : 0);
     if (lane < kBytes / 16)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(row, (lds_byte*)t->row[wave * kRows + j], 16, lane * 16, 0, 0, 0);
   }
 }
 
+// The wave's rows of a code tile as bf16.
 template <int R>
-__device__ __forceinline__ void convert_codes(const CodeTile<R>& g, LatentTile<R>* t, int wave, int lane) {
-  constexpr int kRows = kTok / kAWaves, kChunks = R / 16, kSide = kWave / kChunks;   // rows side by side
+__device__ __forceinline__ void convert_codes(const CodeTile<R>* g, LatentTile<R>* t, int wave, int lane) {
+  constexpr int kChunks = R / 16, kSide = kWave / kChunks;   // rows side by side
 #pragma unroll
   for (int j = 0; j < kRows; j += kSide) {
     const int r = wave * kRows + j + lane / kChunks, c = lane % kChunks;
-    const u4 v = *reinterpret_cast<const u4*>(g.row[r] + c * 16);
-    const float s = *reinterpret_cast<const float*>(g.row[r] + R + 2 * kRope + 4 * (c / 8));
+    const u4 v = *reinterpret_cast<const u4*>(g->row[r] + c * 16);
+    const float s = *reinterpret_cast<const float*>(g->row[r] + R + 2 * kRope + 4 * (c / 8));
     *reinterpret_cast<u4*>(t->c + latent_off<R>(r, 2 * c)) = unpack_fp8(make_uint2(v[0], v[1]), s);
     *reinterpret_cast<u4*>(t->c + latent_off<R>(r, 2 * c + 1)) = unpack_fp8(make_uint2(v[2], v[3]), s);
   }
   if (lane < kRows * 8) {
     const int r = wave * kRows + lane / 8;
     *reinterpret_cast<u4*>(t->r + tile_off<2 * kRope>(r, lane % 8)) =
-        *reinterpret_cast<const u4*>(g.row[r] + R + (lane % 8) * 16);
+        *reinterpret_cast<const u4*>(g->row[r] + R + (lane % 8) * 16);
   }
 }
 
-template <int R, int WQ, int WT, int WD, bool FP8>
-__global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedArgs a) {
-  static_assert(WQ * WT * WD == kAWaves, "waves");
-  constexpr int kSteps = (R + kRope) / 32, kRows = kTok * WT / kAWaves, kStep = kTok * WT;
-  constexpr int kCols = R / WD, kFrags = kCols / 16;   // kFrags is 4 or a multiple of 8
-  constexpr int kQRows = 16 * WQ;
-  // Query operands of the last kQLds steps wait in LDS where the registers do not hold all.
-  constexpr int kQLds = kFrags == 32 ? 8 : 0;
-  __shared__ LatentTile<R> tiles[2][WT];
-  constexpr bool kCodes = FP8 && WT == 1;
-  __shared__ CodeTile<kCodes ? R : 16> codes;
-  __shared__ bf8 qlds[kAWaves][kQLds > 0 ? kQLds : 1][kWave];
-  __shared__ int64_t wsum[kAWaves];
-  __shared__ int64_t found[2];   // the sequence that holds the range's first step, its first step
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int col = lane & 15, grp = lane >> 4;
-  const int wd = wave % WD, wt = wave / WD % WT, wq = wave / (WD * WT);
+// A operand of depth step i (32 values): rows 16 f.. of the tile, cb and rb the lane's
+// offsets at step 0 in the latent and rotary parts.
+template <int R>
+__device__ __forceinline__ bf8 score_row(const LatentTile<R>& t, int cb, int rb, int i, int f) {
+  const uint8_t* k = i < R / 32 ? t.c + f * 16 * 2 * R + (i >> 2) * 256 + (cb ^ ((i & 3) << 6))
+                                : t.r + f * 16 * 2 * kRope + (rb ^ ((i - R / 32) << 6));
+  return *reinterpret_cast<const bf8*>(k);
+}
 
-  // Steps before each sequence, twice: the total fixes the ranges, then the range's first
-  // sequence is looked up.
-  int64_t total = 0;
-  for (int b = tid; b < a.B; b += kAThreads) total += (length_of(a, b) + kStep - 1) / kStep;
+// A operand of 16 value columns (block d from c on): 4 rows a 16-lane group, of both 16-row
+// halves of the tile, read transposed.
+template <int R>
+__device__ __forceinline__ bf8 value_cols(const uint8_t* c, int ct, int d) {
+  typedef __attribute__((address_space(3))) bf4 lds_bf4;
+  const uint8_t* v = c + (d >> 3) * 256 + (ct ^ ((d & 7) << 5));
+  const bf4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf4*)v);
+  const bf4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf4*)(v + 16 * 2 * R));
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// Where a workgroup's range begins: the sequence that holds its first tile and the number
+// of tiles before that sequence; total: tiles of all sequences (one block of query rows).
+struct Range {
+  int b;
+  int64_t before, total;
+};
+
+__device__ __forceinline__ int tiles_of(const AbsorbedArgs& a, int b) { return (length_of(a, b) + kTok - 1) / kTok; }
+
+__device__ __forceinline__ int wave_scan(int v, int lane) {
 #pragma unroll
-  for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o);
-  if (lane == 0) wsum[wave] = total;
-  __syncthreads();
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kAWaves; ++w) total += wsum[w];
-  total = wave_uniform64(total) * a.blocks;
-  const int64_t per = range_steps(total);
-  const int64_t start = blockIdx.x * per, end = min(total, start + per);
-  int64_t before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kAThreads) {
-    const int b = b0 + tid;
-    const int64_t n = b < a.B ? (length_of(a, b) + kStep - 1) / kStep : 0;
-    int64_t incl = n;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int64_t up = __shfl_up(incl, o);
-      if (lane >= o) incl += up;
+  for (int o = 1; o < kWave; o <<= 1) {
+    const int up = __shfl_up(v, o);
+    if (lane >= o) v += up;
+  }
+  return v;
+}
+
+// Workgroup 0 also leaves the sums for the joining kernel.
+// (The kernel has one LDS object: with several, reads of a tile wait for every copy.)
+__device__ __forceinline__ Range find_range(const AbsorbedArgs& a, int* wsum, int* found, int wave, int lane) {
+  Range r{-1, 0, 0};
+  if (a.B <= kWave) {   // each wave by itself
+    const int n = lane < a.B ? tiles_of(a, lane) : 0;
+    const int incl = wave_scan(n, lane);
+    r.total = __builtin_amdgcn_readlane(incl, kWave - 1);
+    const int64_t start = blockIdx.x * range_tiles(r.total * a.blocks);
+    const uint64_t here = __ballot(start >= (int64_t)(incl - n) * a.blocks && start < (int64_t)incl * a.blocks);
+    if (here) {
+      r.b = __builtin_ctzll(here);
+      r.before = __builtin_amdgcn_readlane(incl - n, r.b);
     }
+    if (blockIdx.x == 0 && wave == 0) {
+      if (lane < a.B) a.first[lane] = incl - n;
+      if (lane == a.B - 1) a.first[a.B] = incl;
+    }
+    return r;
+  }
+  // the total first (it fixes the ranges), then the sums, 512 sequences at a time
+  const int tid = wave * kWave + lane;
+  int sum = 0;
+  for (int b = tid; b < a.B; b += kAThreads) sum += tiles_of(a, b);
+  sum = wave_scan(sum, lane);
+  if (lane == kWave - 1) wsum[wave] = sum;
+  if (tid == 0) found[0] = -1;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kAWaves; ++w) r.total += wsum[w];
+  const int64_t start = blockIdx.x * range_tiles(r.total * a.blocks);
+  int before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kAThreads) {
+    const int b = b0 + tid, n = b < a.B ? tiles_of(a, b) : 0;
+    int incl = wave_scan(n, lane);
     __syncthreads();
-    if (lane == 63) wsum[wave] = incl;
+    if (lane == kWave - 1) wsum[wave] = incl;
     __syncthreads();
-    int64_t sum = 0;
+    int all = 0;
     for (int w = 0; w < kAWaves; ++w) {
-      if (w == wave) incl += sum;
-      sum += wsum[w];
+      if (w == wave) incl += all;
+      all += wsum[w];
     }
     incl += before;
     if (b < a.B) {
-      const int64_t lo = (incl - n) * a.blocks;
-      if (start >= lo && start < incl * a.blocks) {
+      if (start >= (int64_t)(incl - n) * a.blocks && start < (int64_t)incl * a.blocks) {
         found[0] = b;
-        found[1] = lo;
+        found[1] = incl - n;
       }
       if (blockIdx.x == 0) {
         a.first[b] = incl - n;
         if (b == a.B - 1) a.first[a.B] = incl;
       }
     }
-    before += sum;
+    before += all;
   }
   __syncthreads();
+  r.b = found[0];
+  r.before = found[1];
+  return r;
+}
+
+template <int R, int WQ, int WD, bool FP8>
+__global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedArgs a) {
+  static_assert(WQ * WD == kAWaves, "waves");
+  using L = Lds<R, WQ, FP8>;
+  constexpr int kSteps = (R + kRope) / 32, kQLds = L::QL;
+  constexpr int kCols = R / WD, kFrags = kCols / 16;   // kFrags is 2, 4 or a multiple of 8
+  constexpr int kQRows = 16 * WQ;
+  __shared__ L lds;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 15, grp = lane >> 4;
+  const int wd = wave % WD, wq = wave / WD;
+
+  const Range range = find_range(a, lds.wsum, lds.found, wave, lane);
+  const int64_t total = wave_uniform64(range.total) * a.blocks, per = range_tiles(total);
+  const int64_t start = blockIdx.x * per, end = min(total, start + per);
   if (start >= total) return;
-  int b = (int)wave_uniform64(found[0]);
-  int64_t seq0 = wave_uniform64(found[1]);
+  int b = __builtin_amdgcn_readfirstlane(range.b);
+  int64_t seq0 = wave_uniform64(range.before) * a.blocks;
 
   const int M = a.Sq * a.H;
   // lane offsets of the tile reads: rows of scores, transposed rows of values
@@ -261,12 +286,12 @@ __global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedAr
   const int ct = (latent_off<R>(4 * grp + (col >> 2), (col & 3) >> 1) + ((col & 1) << 3)) ^ ((wd * kFrags & 7) << 5);
   for (int64_t at = start; at < end;) {
     int len = length_of(a, b);
-    int n = (len + kStep - 1) / kStep;
-    while (at >= seq0 + (int64_t)n * a.blocks) {   // the next sequence with steps
+    int n = (len + kTok - 1) / kTok;
+    while (at >= seq0 + (int64_t)n * a.blocks) {   // the next sequence with tiles
       seq0 += (int64_t)n * a.blocks;
       ++b;
       len = length_of(a, b);
-      n = (len + kStep - 1) / kStep;
+      n = (len + kTok - 1) / kTok;
     }
     const int blk = (int)((at - seq0) / n), t0 = (int)((at - seq0) % n);
     const int t1 = (int)min((int64_t)n, t0 + (end - at));
@@ -276,6 +301,29 @@ __global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedAr
     // rows that this lane's query sees
     const int limit = len - (a.Sq - 1 - min(row, M - 1) / a.H);
 
+    // cache rows of the next kBatch tiles to copy, kRows lanes a tile; pages a batch ahead
+    auto page_at = [&](int t) {
+      const int pos = (t + lane / kRows) * kTok + wave * kRows + lane % kRows;
+      const uint32_t p = min((uint32_t)pos / (uint32_t)a.page, (uint32_t)(a.max_pages - 1));
+      return a.table[(int64_t)b * a.max_pages + p];
+    };
+    auto slots_at = [&](int pg, int t) {
+      const int tile = t + lane / kRows, pos = tile * kTok + wave * kRows + lane % kRows;
+      const bool there = tile < t1 && pos < len && pg >= 0 && pg < a.n_pages;
+      return there ? pg * a.page + (int)((uint32_t)pos % (uint32_t)a.page) : -1;
+    };
+    int batch = t0, slots = slots_at(page_at(t0), t0), pages = page_at(t0 + kBatch);
+    // copies of tile t (past t1: of nothing); t goes up by one from call to call
+    auto copy = [&](LatentTile<R>* to, CodeTile<FP8 ? R : 16>* codes, int t) __attribute__((always_inline)) {
+      if (t - batch == kBatch) {
+        batch = t;
+        slots = slots_at(pages, t);
+        pages = page_at(t + kBatch);
+      }
+      if constexpr (FP8) copy_codes<R>(a, codes, slots, (t - batch) * kRows, wave, lane);
+      else copy_rows<R>(a, to, slots, (t - batch) * kRows, wave, lane);
+    };
+
     bf8 qf[kSteps - kQLds];
     {
       const uint16_t* qp = a.q + ((int64_t)b * M + min(row, M - 1)) * (R + kRope) + 8 * grp;
@@ -283,163 +331,123 @@ __global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedAr
       for (int s = 0; s < kSteps - kQLds; ++s) qf[s] = *reinterpret_cast<const bf8*>(qp + 32 * s);
 #pragma unroll
       for (int s = 0; s < kQLds; ++s)
-        qlds[wave][s][lane] = *reinterpret_cast<const bf8*>(qp + 32 * (kSteps - kQLds + s));
+        lds.q[wave][s][lane] = *reinterpret_cast<const bf8*>(qp + 32 * (kSteps - kQLds + s));
     }
     f4 o[kFrags];
 #pragma unroll
     for (int d = 0; d < kFrags; ++d) o[d] = f4{0.0f, 0.0f, 0.0f, 0.0f};
     float m = kNegInf, l = 0.0f;
 
-    Stage<R, WT, FP8> stage;
-    const int mine = wave * kRows + min(lane, kRows - 1);
-    auto pos_of = [&](int t) { return t * kStep + mine; };
-    // The copies of step t + 1 go to `next` while `cur` is worked on: the pointers are
-    // declared not to alias, or the reads of `cur` would wait for them.
-    auto step = [&](const LatentTile<R>* __restrict__ cur, LatentTile<R>* __restrict__ next, int t,
-                    int& pg) __attribute__((always_inline)) {
-      if constexpr (kCodes) {
-        if (t + 1 < t1) convert_codes<R>(codes, next, wave, lane);
-        if (t + 2 < t1) {
-          copies_done();   // the codes are read before the next ones land on them
-          copy_codes<R>(a, &codes, row_slot(a, pg, pos_of(t + 2), len), wave, lane);
-          pg = page_of(a, b, pos_of(t + 3));
-        }
+    // One tile. `far` and `codes` are written by copies while `cur` is read, `next` by the
+    // conversion: the pointers are declared not to alias, or the reads would wait.
+    auto step = [&](const LatentTile<R>* __restrict__ cur, LatentTile<R>* __restrict__ next,
+                    LatentTile<R>* __restrict__ far, CodeTile<FP8 ? R : 16>* __restrict__ codes,
+                    int t) __attribute__((always_inline)) {
+      if constexpr (FP8) {
+        convert_codes<R>(codes, next, wave, lane);
+        __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0): the codes are read before others land on them
+        copy(nullptr, codes, t + L::kAhead);
       } else {
-        if (t + 1 < t1) load_rows<R, WT, FP8>(a, stage, next, row_slot(a, pg, pos_of(t + 1), len), wave, lane);
-        if (t + 2 < t1) pg = page_of(a, b, pos_of(t + 2));
+        copy(far, nullptr, t + L::kAhead);
       }
-      const LatentTile<R>& tl = cur[wt];
-      const int p0 = t * kStep + wt * kTok;   // position of the tile's first row
-      if (busy && p0 < len) {
-        f4 s[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-        // Row reads run kAhead products' worth ahead; the scheduling barriers keep them
-        // there (left alone, every product waits for its own read).
-        auto row_at = [&](int i, int f) {
-          const uint8_t* k = i < R / 32 ? tl.c + f * 16 * 2 * R + (i >> 2) * 256 + (cb ^ ((i & 3) << 6))
-                                        : tl.r + f * 16 * 2 * kRope + (rb ^ ((i - R / 32) << 6));
-          return *reinterpret_cast<const bf8*>(k);
-        };
-        auto q_at = [&](int i) { return i < kSteps - kQLds ? qf[i] : qlds[wave][i - (kSteps - kQLds)][lane]; };
-        bf8 kf[kAhead][2], qn[2] = {q_at(0), q_at(1)};
+      const int p0 = t * kTok;   // position of the tile's first row
+      if (!busy) return;
+      f4 s[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+      // Row reads run kAhead steps ahead of their products; the scheduling barriers keep them
+      // there (left alone, every product waits for its own read).
+      auto q_at = [&](int i) { return i < kSteps - kQLds ? qf[i] : lds.q[wave][i - (kSteps - kQLds)][lane]; };
+      bf8 kf[kAhead][2], qn[2] = {q_at(0), q_at(1)};
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) kf[i][0] = row_at(i, 0), kf[i][1] = row_at(i, 1);
+      for (int i = 0; i < kAhead; ++i) kf[i][0] = score_row<R>(*cur, cb, rb, i, 0), kf[i][1] = score_row<R>(*cur, cb, rb, i, 1);
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-          __builtin_amdgcn_sched_barrier(0);
-          const bf8 q = qn[i % 2];
-          s[0] = mfma16(kf[i % kAhead][0], q, s[0]);
-          s[1] = mfma16(kf[i % kAhead][1], q, s[1]);
-          if (i + 2 < kSteps) qn[i % 2] = q_at(i + 2);
-          if (i + kAhead < kSteps) {
-            kf[i % kAhead][0] = row_at(i + kAhead, 0);
-            kf[i % kAhead][1] = row_at(i + kAhead, 1);
-          }
-        }
+      for (int i = 0; i < kSteps; ++i) {
         __builtin_amdgcn_sched_barrier(0);
-        const bool edge = p0 + kTok > len - (a.Sq - 1);
-        float top = kNegInf;
+        const bf8 q = qn[i % 2];
+        s[0] = mfma16(kf[i % kAhead][0], q, s[0]);
+        s[1] = mfma16(kf[i % kAhead][1], q, s[1]);
+        if (i + 2 < kSteps) qn[i % 2] = q_at(i + 2);
+        if (i + kAhead < kSteps) {
+          kf[i % kAhead][0] = score_row<R>(*cur, cb, rb, i + kAhead, 0);
+          kf[i % kAhead][1] = score_row<R>(*cur, cb, rb, i + kAhead, 1);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      constexpr int kVAhead = kQLds > 0 ? 4 : kFrags < 6 ? kFrags : 6;
+      bf8 vf[kVAhead];
+#pragma unroll
+      for (int d = 0; d < kVAhead; ++d) vf[d] = value_cols<R>(cur->c + (wd * kFrags >> 3) * 256, ct, d);
+      __builtin_amdgcn_sched_barrier(0);
+      if (p0 + kTok > len - (a.Sq - 1)) {   // some query hides some row
 #pragma unroll
         for (int f = 0; f < 2; ++f)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            float x = s[f][r] * a.scale2;
-            if (edge) x = p0 + 16 * f + 4 * grp + r < limit ? x : kNegInf;
-            s[f][r] = x;
-            top = fmaxf(top, x);
-          }
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = half_max(top);
-        // The running reference moves only when a score passes it by kSlack: the weights
-        // stay below 2^kSlack, exact in FP32's and bf16's range, and the sums are seldom
-        // rescaled. The first score of a row always sets it.
-        const bool moved = top > m + kSlack || (m == kNegInf && top > kNegInf);
-        if (__any(moved)) {
-          const float to = moved ? top : m;
-          const float shrink = to == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - to);
-          m = to;
-          l *= shrink;
+          for (int r = 0; r < 4; ++r) s[f][r] = p0 + 16 * f + 4 * grp + r < limit ? s[f][r] : kNegInf;
+      }
+      float top = kNegInf;
 #pragma unroll
-          for (int d = 0; d < kFrags; ++d) o[d] *= shrink;
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) top = fmaxf(top, s[f][r]);
+      top = half_max(row_max(top)) * a.scale2;
+      // The reference of a row (m, in log2) moves only when a score passes it by kSlack: the
+      // weights stay below 2^kSlack, and O is seldom rescaled. A row's first score sets it.
+      const bool moved = top > m + kSlack || (m == kNegInf && top > kNegInf);
+      if (__any(moved)) {
+        const float to = moved ? top : m;
+        const float shrink = to == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+        m = to;
+        l *= shrink;
+#pragma unroll
+        for (int d = 0; d < kFrags; ++d) o[d] *= shrink;
+      }
+      const float base = m == kNegInf ? 0.0f : m;
+      union { uint32_t u[4]; bf8 v; } p;
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          s[f][r] = __builtin_amdgcn_exp2f(fmaf(s[f][r], a.scale2, -base));
+          l += s[f][r];
         }
-        const float base = m == kNegInf ? 0.0f : m;
+        p.u[2 * f] = pack_bf16x2(s[f][0], s[f][1]);
+        p.u[2 * f + 1] = pack_bf16x2(s[f][2], s[f][3]);
+      }
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            s[f][r] = __builtin_amdgcn_exp2f(s[f][r] - base);
-            l += s[f][r];
-          }
-        union { uint32_t u[4]; bf8 v; } p;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) p.u[i] = pack_bf16x2(s[i / 2][2 * (i % 2)], s[i / 2][2 * (i % 2) + 1]);
-        auto col_at = [&](int d) {
-          // columns 16 (wd * kFrags + d)..: 4 rows a 16-lane group, of both 16-row halves
-          typedef __attribute__((address_space(3))) bf4 lds_bf4;
-          const uint8_t* v = tl.c + ((wd * kFrags >> 3) + (d >> 3)) * 256 + (ct ^ ((d & 7) << 5));
-          const bf4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf4*)v);
-          const bf4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf4*)(v + 16 * 2 * R));
-          return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        };
-        constexpr int kVAhead = kFrags < 6 ? kFrags : 6;
-        bf8 vf[kVAhead];
-#pragma unroll
-        for (int d = 0; d < kVAhead; ++d) vf[d] = col_at(d);
-#pragma unroll
-        for (int d = 0; d < kFrags; ++d) {
-          __builtin_amdgcn_sched_barrier(0);
-          o[d] = mfma16(vf[d % kVAhead], p.v, o[d]);
-          if (d + kVAhead < kFrags) vf[d % kVAhead] = col_at(d + kVAhead);
-        }
+      for (int d = 0; d < kFrags; ++d) {
         __builtin_amdgcn_sched_barrier(0);
+        o[d] = mfma16(vf[d % kVAhead], p.v, o[d]);
+        if (d + kVAhead < kFrags) vf[d % kVAhead] = value_cols<R>(cur->c + (wd * kFrags >> 3) * 256, ct, d + kVAhead);
       }
-      if constexpr (FP8 && !kCodes) {
-        if (t + 1 < t1) store_rows<R, WT>(stage, next, wave, lane);
-      }
+      __builtin_amdgcn_sched_barrier(0);
     };
 
-    int pg = page_of(a, b, pos_of(t0));
-    if constexpr (kCodes) {
-      copy_codes<R>(a, &codes, row_slot(a, pg, pos_of(t0), len), wave, lane);
-      pg = page_of(a, b, pos_of(t0 + 1));
+    // the first tiles' copies
+    if constexpr (FP8) {
+      copy(nullptr, &lds.code[0], t0);
       copies_done();
-      convert_codes<R>(codes, tiles[t0 & 1], wave, lane);
+      convert_codes<R>(&lds.code[0], &lds.tile[0], wave, lane);
       copies_done();
-      if (t0 + 1 < t1) copy_codes<R>(a, &codes, row_slot(a, pg, pos_of(t0 + 1), len), wave, lane);
-      pg = page_of(a, b, pos_of(t0 + 2));
+#pragma unroll
+      for (int i = 1; i <= L::NC; ++i) copy(nullptr, &lds.code[i % L::NC], t0 + i);
     } else {
-      load_rows<R, WT, FP8>(a, stage, tiles[t0 & 1], row_slot(a, pg, pos_of(t0), len), wave, lane);
-      if constexpr (FP8) store_rows<R, WT>(stage, tiles[t0 & 1], wave, lane);
-      pg = page_of(a, b, pos_of(t0 + 1));
-    }
-    for (int t = t0; t < t1; ++t) {
-      copies_done_barrier();
-      step(tiles[t & 1], tiles[(t + 1) & 1], t, pg);
-    }
-    l += __shfl_xor(l, 16);
-    l = half_sum(l);
-    if constexpr (WT == 2) {   // the second tile's waves hand their part to the first's
-      copies_done_barrier();
-      f4* x = reinterpret_cast<f4*>(tiles) + (wq * WD + wd) * kFrags * 64 + lane;
-      float* ml = reinterpret_cast<float*>(reinterpret_cast<f4*>(tiles) + WQ * WD * kFrags * 64);
-      static_assert(WQ * WD * (kFrags * 1024 + 512) <= (int)sizeof(tiles), "hand-over fits the tiles");
-      if (wt == 1) {
 #pragma unroll
-        for (int d = 0; d < kFrags; ++d) x[d * 64] = o[d];
-        ml[(wq * WD + wd) * 128 + lane] = m;
-        ml[(wq * WD + wd) * 128 + 64 + lane] = l;
-      }
-      copies_done_barrier();
-      if (wt == 0) {
-        const float m1 = ml[(wq * WD + wd) * 128 + lane], l1 = ml[(wq * WD + wd) * 128 + 64 + lane];
-        const float top = fmaxf(m, m1), base = top == kNegInf ? 0.0f : top;
-        const float w0 = __builtin_amdgcn_exp2f(m - base), w1 = __builtin_amdgcn_exp2f(m1 - base);
-        m = top;
-        l = l * w0 + l1 * w1;
-#pragma unroll
-        for (int d = 0; d < kFrags; ++d) o[d] = o[d] * w0 + x[d * 64] * w1;
-      }
+      for (int i = 0; i < L::kAhead; ++i) copy(&lds.tile[i], nullptr, t0 + i);
     }
-    if (busy && wt == 0) {
+    // the query operands have arrived (or each tile's first product would wait for all copies)
+#pragma unroll
+    for (int i = 0; i < kSteps - kQLds; ++i) asm volatile("" : "+v"(qf[i]));
+    for (int t = t0, k = 0; t < t1; ++t, ++k) {
+      // bf16: tile t has landed; E4M3: tile t is converted and the codes of t + 1 have landed.
+      // Every wave is done with tile t - 1.
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(L::kCopies * (L::kAhead - 1 - FP8)));
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      step(&lds.tile[k % L::NT], &lds.tile[(k + 1) % L::NT], &lds.tile[(k + L::NT - 1) % L::NT],
+           &lds.code[FP8 ? (k + 1) % max(L::NC, 1) : 0], t);
+    }
+    l = half_sum(row_sum(l));
+    if (busy) {
       if (whole) {
         if (row < M) {
           const float inv = l > 0.0f ? 1.0f / l : 0.0f;
@@ -463,43 +471,74 @@ __global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedAr
       }
     }
     at += t1 - t0;
-    copies_done_barrier();   // every wave is done with the tiles before the next block's
+    copies_done_barrier();   // every wave is done with the buffers before the next block's copies
   }
 }
 
 // Joins the partial results of a block of query rows, or writes the empty result of a
-// sequence without rows. A workgroup takes 16 query rows; a thread 4 columns at a time.
+// sequence without rows. A workgroup takes 16 query rows and 64 columns; its waves take
+// every fourth partial result each, then 16 columns each of the four waves' sums.
+constexpr int kJoinWaves = 4;
+
 template <int R, int WQ>
-__global__ __launch_bounds__(256) void absorbed_join_kernel(const AbsorbedArgs a) {
+__global__ __launch_bounds__(kJoinWaves* kWave) void absorbed_join_kernel(const AbsorbedArgs a) {
   constexpr int kQRows = 16 * WQ;
+  __shared__ f4 osum[kJoinWaves][4][kWave];
+  __shared__ float msum[kJoinWaves][16], lsum[kJoinWaves][16];
   const int unit = blockIdx.x;
   const int wq = unit % WQ, blk = unit / WQ % a.blocks, b = unit / WQ / a.blocks;
-  const int lane = threadIdx.x & 63, col = lane & 15, grp = lane >> 4;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, grp = lane >> 4;
   const int M = a.Sq * a.H, row = blk * kQRows + wq * 16 + col;
   const int64_t n = a.first[b + 1] - a.first[b];
   const int64_t s0 = a.first[b] * a.blocks + blk * n, s1 = s0 + n;
-  const int64_t per = range_steps(a.first[a.B] * a.blocks);
+  const int64_t per = range_tiles(a.first[a.B] * a.blocks);
   const int64_t g0 = s0 / per, g1 = n > 0 ? (s1 - 1) / per : g0 - 1;
-  if (g0 == g1 || row >= M) return;
+  if (g0 == g1 || blk * kQRows + wq * 16 >= M) return;   // one range had all of it, or no query row
   auto part = [&](int64_t g) { return a.part + (g * 2 + (s0 <= g * per ? 0 : 1)) * part_floats(R, kQRows); };
-  float m = kNegInf;
-  for (int64_t g = g0; g <= g1; ++g) m = fmaxf(m, part(g)[kQRows * R + wq * 16 + col]);
-  const float base = m == kNegInf ? 0.0f : m;
-  const int d = blockIdx.y * 4 + (threadIdx.x >> 6);
-  float l = 0.0f;
-  f4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto weights = [&](int64_t g) { return part(g) + kQRows * R + wq * 16 + col; };
+  float m = kNegInf, l = 0.0f;
 #pragma unroll 4
-  for (int64_t g = g0; g <= g1; ++g) {
-    const float* p = part(g);
-    const float w = __builtin_amdgcn_exp2f(p[kQRows * R + wq * 16 + col] - base);
-    l = fmaf(w, p[kQRows * (R + 1) + wq * 16 + col], l);
-    const f4 v = *reinterpret_cast<const f4*>(p + ((wq * (R / 16) + d) * 64 + lane) * 4);
+  for (int64_t g = g0 + wave; g <= g1; g += kJoinWaves) m = fmaxf(m, *weights(g));
+  const float base = m == kNegInf ? 0.0f : m;
+  f4 o[4] = {};
+#pragma unroll 2
+  for (int64_t g = g0 + wave; g <= g1; g += kJoinWaves) {
+    const float w = __builtin_amdgcn_exp2f(*weights(g) - base);
+    l = fmaf(w, weights(g)[kQRows], l);
+    const f4* p = reinterpret_cast<const f4*>(part(g)) + (wq * (R / 16) + blockIdx.y * 4) * kWave + lane;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = fmaf(w, v[e], o[e]);
+    for (int d = 0; d < 4; ++d) {
+      const f4 v = p[d * kWave];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[d][e] = fmaf(w, v[e], o[d][e]);
+    }
   }
+#pragma unroll
+  for (int d = 0; d < 4; ++d) osum[wave][d][lane] = o[d];
+  if (grp == 0) {
+    msum[wave][col] = m;
+    lsum[wave][col] = l;
+  }
+  __syncthreads();
+  m = kNegInf;
+#pragma unroll
+  for (int w = 0; w < kJoinWaves; ++w) m = fmaxf(m, msum[w][col]);
+  const float top = m == kNegInf ? 0.0f : m;
+  l = 0.0f;
+  f4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int w = 0; w < kJoinWaves; ++w) {
+    const float f = __builtin_amdgcn_exp2f(msum[w][col] - top);
+    l = fmaf(f, lsum[w][col], l);
+    const f4 v = osum[w][wave][lane];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] = fmaf(f, v[e], sum[e]);
+  }
+  if (row >= M) return;
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-  store4(a.out, ((int64_t)b * M + row) * R + 16 * d + 4 * grp, a.out_bf16, o[0] * inv, o[1] * inv, o[2] * inv,
-         o[3] * inv);
+  const int d = blockIdx.y * 4 + wave;
+  store4(a.out, ((int64_t)b * M + row) * R + 16 * d + 4 * grp, a.out_bf16, sum[0] * inv, sum[1] * inv, sum[2] * inv,
+         sum[3] * inv);
   if (d == 0 && grp == 0)
     a.lse[(int64_t)b * M + row] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : kNegInf;
 }
@@ -508,20 +547,22 @@ __global__ __launch_bounds__(256) void absorbed_join_kernel(const AbsorbedArgs a
 int query_rows(int M) { return M > 64 ? 128 : M > 32 ? 64 : M > 16 ? 32 : 16; }
 size_t first_bytes(int64_t B) { return ((size_t)(B + 1) * 8 + 255) / 256 * 256; }
 
-template <int R, int WQ, int WT, int WD>
+template <int R, int WQ>
 void launch_absorbed(const AbsorbedArgs& a, bool fp8, hipStream_t s) {
-  if (fp8) hipLaunchKernelGGL((absorbed_kernel<R, WQ, WT, WD, true>), dim3(kGroups), dim3(kAThreads), 0, s, a);
-  else hipLaunchKernelGGL((absorbed_kernel<R, WQ, WT, WD, false>), dim3(kGroups), dim3(kAThreads), 0, s, a);
-  hipLaunchKernelGGL((absorbed_join_kernel<R, WQ>), dim3((unsigned)(a.B * a.blocks * WQ), R / 64), dim3(256), 0, s, a);
+  constexpr int WD = kAWaves / WQ;
+  if (fp8) hipLaunchKernelGGL((absorbed_kernel<R, WQ, WD, true>), dim3(kGroups), dim3(kAThreads), 0, s, a);
+  else hipLaunchKernelGGL((absorbed_kernel<R, WQ, WD, false>), dim3(kGroups), dim3(kAThreads), 0, s, a);
+  hipLaunchKernelGGL((absorbed_join_kernel<R, WQ>), dim3((unsigned)(a.B * a.blocks * WQ), R / 64),
+                     dim3(kJoinWaves * kWave), 0, s, a);
 }
 
 template <int R>
 void launch_rows(const AbsorbedArgs& a, bool fp8, hipStream_t s) {
   switch (query_rows(a.Sq * a.H)) {
-    case 16: return launch_absorbed<R, 1, 2, 4>(a, fp8, s);
-    case 32: return launch_absorbed<R, 2, 2, 2>(a, fp8, s);
-    case 64: return launch_absorbed<R, 4, 1, 2>(a, fp8, s);
-    default: return launch_absorbed<R, 8, 1, 1>(a, fp8, s);
+    case 16: return launch_absorbed<R, 1>(a, fp8, s);
+    case 32: return launch_absorbed<R, 2>(a, fp8, s);
+    case 64: return launch_absorbed<R, 4>(a, fp8, s);
+    default: return launch_absorbed<R, 8>(a, fp8, s);
   }
 }
 
@@ -560,7 +601,8 @@ extern "C" moe_status moe_latent_attn_absorbed(const moe_latent_config* cfg, int
                        reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + first_bytes(B)), n_pages, max_pages,
                        (int)B, Sq, cfg->n_heads, page_size, (M + query_rows(M) - 1) / query_rows(M), scale * kLog2e,
                        ot == MOE_BF16};
-  if ((int64_t)a.B * a.blocks * 8 > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)a.B * a.blocks * 8 > 0x7fffffff || max_pages * page_size / kTok * B > 0x7fff0000)
+    return MOE_ERR_UNSUPPORTED;   // 32-bit counts of tiles
   const bool fp8 = cfg->cache_kind == MOE_CACHE_FP8;
   if (cfg->latent == 512) launch_rows<512>(a, fp8, as_stream(stream));
   else launch_rows<256>(a, fp8, as_stream(stream));
