@@ -40,7 +40,7 @@ struct AbsorbedArgs {
   const int32_t *table, *lengths;
   void* out;
   float* lse;
-  int64_t* first;      // [B + 1]: tiles before each sequence (one block of query rows)
+  int64_t* first;      // [B + 2]: tiles before each sequence (one block of query rows); tiles of a range
   float* part;         // [kGroups][2] partial results
   int64_t n_pages, max_pages;
   int B, Sq, H, page, blocks;   // blocks of query rows a sequence
@@ -55,8 +55,15 @@ __device__ __forceinline__ f4 mfma16(bf8 a, bf8 b, f4 c) {
 __device__ __forceinline__ int length_of(const AbsorbedArgs& a, int b) {
   return (int)min((int64_t)max(a.lengths[b], 0), a.max_pages * a.page);
 }
-__device__ __forceinline__ int64_t range_tiles(int64_t total) {
-  return max((int64_t)kMinTiles, (total + kGroups - 1) / kGroups);
+// Tiles of a range, for `total` tiles of all sequences (one block of query rows). At least as
+// many as the workgroups need; for few long sequences more, since the parts of a block of
+// query rows are joined one after another by the waves of one workgroup: n tiles a block
+// cost n / g for the join and g for the range, least at g ~ sqrt(n) (one sequence of 20000
+// rows, 16 heads: 39 us at 3 tiles, 32 at 7).
+__device__ __forceinline__ int64_t range_tiles(const AbsorbedArgs& a, int64_t total) {
+  const int64_t even = (total * a.blocks + kGroups - 1) / kGroups;
+  const int64_t few = (int64_t)sqrtf((float)total / (float)a.B * 0.1f);
+  return max(max((int64_t)kMinTiles, even), few);
 }
 // floats of a partial result of n query rows: O, then the maxima and the sums
 __host__ __device__ constexpr int64_t part_floats(int latent, int n) { return (int64_t)n * (latent + 2); }
@@ -181,10 +188,11 @@ __device__ __forceinline__ bf8 value_cols(const uint8_t* c, int ct, int d) {
 }
 
 // Where a workgroup's range begins: the sequence that holds its first tile and the number
-// of tiles before that sequence; total: tiles of all sequences (one block of query rows).
+// of tiles before that sequence; total: tiles of all sequences (one block of query rows);
+// per: tiles of a range.
 struct Range {
   int b;
-  int64_t before, total;
+  int64_t before, total, per;
 };
 
 __device__ __forceinline__ int tiles_of(const AbsorbedArgs& a, int b) { return (length_of(a, b) + kTok - 1) / kTok; }
@@ -201,12 +209,13 @@ __device__ __forceinline__ int wave_scan(int v, int lane) {
 // Workgroup 0 also leaves the sums for the joining kernel.
 // (The kernel has one LDS object: with several, reads of a tile wait for every copy.)
 __device__ __forceinline__ Range find_range(const AbsorbedArgs& a, int* wsum, int* found, int wave, int lane) {
-  Range r{-1, 0, 0};
+  Range r{-1, 0, 0, 0};
   if (a.B <= kWave) {   // each wave by itself
     const int n = lane < a.B ? tiles_of(a, lane) : 0;
     const int incl = wave_scan(n, lane);
     r.total = __builtin_amdgcn_readlane(incl, kWave - 1);
-    const int64_t start = blockIdx.x * range_tiles(r.total * a.blocks);
+    r.per = range_tiles(a, r.total);
+    const int64_t start = blockIdx.x * r.per;
     const uint64_t here = __ballot(start >= (int64_t)(incl - n) * a.blocks && start < (int64_t)incl * a.blocks);
     if (here) {
       r.b = __builtin_ctzll(here);
@@ -214,7 +223,10 @@ __device__ __forceinline__ Range find_range(const AbsorbedArgs& a, int* wsum, in
     }
     if (blockIdx.x == 0 && wave == 0) {
       if (lane < a.B) a.first[lane] = incl - n;
-      if (lane == a.B - 1) a.first[a.B] = incl;
+      if (lane == a.B - 1) {
+        a.first[a.B] = incl;
+        a.first[a.B + 1] = r.per;
+      }
     }
     return r;
   }
@@ -228,7 +240,8 @@ __device__ __forceinline__ Range find_range(const AbsorbedArgs& a, int* wsum, in
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kAWaves; ++w) r.total += wsum[w];
-  const int64_t start = blockIdx.x * range_tiles(r.total * a.blocks);
+  r.per = range_tiles(a, r.total);
+  const int64_t start = blockIdx.x * r.per;
   int before = 0;
   for (int b0 = 0; b0 < a.B; b0 += kAThreads) {
     const int b = b0 + tid, n = b < a.B ? tiles_of(a, b) : 0;
@@ -249,7 +262,10 @@ __device__ __forceinline__ Range find_range(const AbsorbedArgs& a, int* wsum, in
       }
       if (blockIdx.x == 0) {
         a.first[b] = incl - n;
-        if (b == a.B - 1) a.first[a.B] = incl;
+        if (b == a.B - 1) {
+          a.first[a.B] = incl;
+          a.first[a.B + 1] = r.per;
+        }
       }
     }
     before += all;
@@ -273,7 +289,7 @@ __global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedAr
   const int wd = wave % WD, wq = wave / WD;
 
   const Range range = find_range(a, lds.wsum, lds.found, wave, lane);
-  const int64_t total = wave_uniform64(range.total) * a.blocks, per = range_tiles(total);
+  const int64_t total = wave_uniform64(range.total) * a.blocks, per = wave_uniform64(range.per);
   const int64_t start = blockIdx.x * per, end = min(total, start + per);
   if (start >= total) return;
   int b = __builtin_amdgcn_readfirstlane(range.b);
@@ -491,27 +507,26 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void absorbed_join_kernel(const 
   const int M = a.Sq * a.H, row = blk * kQRows + wq * 16 + col;
   const int64_t n = a.first[b + 1] - a.first[b];
   const int64_t s0 = a.first[b] * a.blocks + blk * n, s1 = s0 + n;
-  const int64_t per = range_tiles(a.first[a.B] * a.blocks);
+  const int64_t per = a.first[a.B + 1];
   const int64_t g0 = s0 / per, g1 = n > 0 ? (s1 - 1) / per : g0 - 1;
   if (g0 == g1 || blk * kQRows + wq * 16 >= M) return;   // one range had all of it, or no query row
   auto part = [&](int64_t g) { return a.part + (g * 2 + (s0 <= g * per ? 0 : 1)) * part_floats(R, kQRows); };
-  auto weights = [&](int64_t g) { return part(g) + kQRows * R + wq * 16 + col; };
   float m = kNegInf, l = 0.0f;
-#pragma unroll 4
-  for (int64_t g = g0 + wave; g <= g1; g += kJoinWaves) m = fmaxf(m, *weights(g));
-  const float base = m == kNegInf ? 0.0f : m;
   f4 o[4] = {};
 #pragma unroll 2
   for (int64_t g = g0 + wave; g <= g1; g += kJoinWaves) {
-    const float w = __builtin_amdgcn_exp2f(*weights(g) - base);
-    l = fmaf(w, weights(g)[kQRows], l);
-    const f4* p = reinterpret_cast<const f4*>(part(g)) + (wq * (R / 16) + blockIdx.y * 4) * kWave + lane;
+    const float* p = part(g);
+    const float mg = p[kQRows * R + wq * 16 + col], lg = p[kQRows * (R + 1) + wq * 16 + col];
+    const f4* og = reinterpret_cast<const f4*>(p) + (wq * (R / 16) + blockIdx.y * 4) * kWave + lane;
+    const f4 v[4] = {og[0], og[kWave], og[2 * kWave], og[3 * kWave]};
+    const float top = fmaxf(m, mg), base = top == kNegInf ? 0.0f : top;
+    const float f0 = __builtin_amdgcn_exp2f(m - base), f1 = __builtin_amdgcn_exp2f(mg - base);
+    m = top;
+    l = l * f0 + lg * f1;
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-      const f4 v = p[d * kWave];
+    for (int d = 0; d < 4; ++d)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[d][e] = fmaf(w, v[e], o[d][e]);
-    }
+      for (int e = 0; e < 4; ++e) o[d][e] = fmaf(f1, v[d][e], o[d][e] * f0);
   }
 #pragma unroll
   for (int d = 0; d < 4; ++d) osum[wave][d][lane] = o[d];
@@ -545,7 +560,7 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void absorbed_join_kernel(const 
 
 // Query rows of a workgroup: as many 16-row groups as the query has, up to 8.
 int query_rows(int M) { return M > 64 ? 128 : M > 32 ? 64 : M > 16 ? 32 : 16; }
-size_t first_bytes(int64_t B) { return ((size_t)(B + 1) * 8 + 255) / 256 * 256; }
+size_t first_bytes(int64_t B) { return ((size_t)(B + 2) * 8 + 255) / 256 * 256; }
 
 template <int R, int WQ>
 void launch_absorbed(const AbsorbedArgs& a, bool fp8, hipStream_t s) {
