@@ -32,6 +32,20 @@ struct __attribute__((aligned(256))) KvTile {
   uint8_t k[kKeys * 2 * D], r[kKeys * 2 * kRope], v[kKeys * 2 * D];
 };
 
+constexpr int kAhead = 6;   // products that an LDS read runs ahead
+
+// A operand of product i of the scores: 32 keys i % 2, depth step i / 2 (the rotary part last).
+template <int D>
+__device__ __forceinline__ bf8 score_row(const KvTile<D>& t, int kb, int rb, int i) {
+  const int f = 32 * (i % 2), s = i / 2;
+  return s < D / 16 ? row_frag<2 * D>(t.k, kb, f, s) : row_frag<2 * kRope>(t.r, rb, f, s - D / 16);
+}
+// A operand of product i of the values: 16 keys i / (D / 32), column block i % (D / 32).
+template <int D>
+__device__ __forceinline__ bf8 value_cols(const KvTile<D>& t, int vb, int i) {
+  return tr_frag<2 * D>(t.v, vb, 16 * (i / (D / 32)), i % (D / 32));
+}
+
 template <int D>
 __device__ __forceinline__ void copy_kv(const ExpandedArgs& a, KvTile<D>* t, int64_t key0, int n, int h, int wave,
                                         int lane) {
@@ -105,16 +119,20 @@ __global__ __launch_bounds__(kFWaves* PARTS* kWave, 2) void expanded_kernel(cons
     const int k0 = t * kKeys;
     copy(next, t + PARTS);
     if (PARTS > 1 && t >= n_tiles) return;
-    f16v s[kKeys / 32];
+    // Products laid out by hand, a scheduling barrier after each: LDS reads run kAhead
+    // products ahead of the one that takes them.
+    f16v s[2] = {zero16(), zero16()};
+    bf8 rows[kAhead], cols[kAhead];
 #pragma unroll
-    for (int f = 0; f < kKeys / 32; ++f) {
-      s[f] = zero16();
+    for (int i = 0; i < kAhead; ++i) rows[i] = score_row<D>(*cur, kb, rb, i);
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) s[f] = mfma(row_frag<2 * D>(cur->k, kb, 32 * f, i), qf[i], s[f]);
-#pragma unroll
-      for (int i = 0; i < kRope / 16; ++i)
-        s[f] = mfma(row_frag<2 * kRope>(cur->r, rb, 32 * f, i), qf[D / 16 + i], s[f]);
+    for (int i = 0; i < 2 * kSteps; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+      s[i % 2] = mfma(rows[i % kAhead], qf[i / 2], s[i % 2]);
+      if (i + kAhead < 2 * kSteps) rows[i % kAhead] = score_row<D>(*cur, kb, rb, i + kAhead);
+      else cols[i + kAhead - 2 * kSteps] = value_cols<D>(*cur, vb, i + kAhead - 2 * kSteps);
     }
+    __builtin_amdgcn_sched_barrier(0);
     if (k0 + kKeys > (a.causal ? min(nk, w0 + nk - nq + 1) : nk)) {   // some query hides some key
 #pragma unroll
       for (int f = 0; f < kKeys / 32; ++f)
@@ -142,17 +160,29 @@ __global__ __launch_bounds__(kFWaves* PARTS* kWave, 2) void expanded_kernel(cons
         for (int r = 0; r < 16; ++r) o[d][r] *= shrink;
     }
     const float base = m == kNegInf ? 0.0f : m;
+    // weights of 16 keys, then the products of the 16 before beside the next ones' weights
+    auto weight = [&](float x) __attribute__((always_inline)) {
+      x = __builtin_amdgcn_exp2f(fmaf(x, a.scale2, -base));
+      l += x;
+      return x;
+    };
 #pragma unroll
-    for (int ks = 0; ks < kKeys / 16; ++ks) {
+    for (int r = 0; r < 8; ++r) s[0][r] = weight(s[0][r]);
+    bf8 p = b_operand(s[0], 0);
+    constexpr int kBlocks = D / 32, kPer = 8 / kBlocks;
 #pragma unroll
-      for (int r = 8 * (ks % 2); r < 8 * (ks % 2) + 8; ++r) {
-        s[ks / 2][r] = __builtin_amdgcn_exp2f(fmaf(s[ks / 2][r], a.scale2, -base));
-        l += s[ks / 2][r];
+    for (int i = 0; i < 4 * kBlocks; ++i) {
+      const int ks = i / kBlocks, d = i % kBlocks;
+      __builtin_amdgcn_sched_barrier(0);
+      o[d] = mfma(cols[i % kAhead], p, o[d]);
+      if (i + kAhead < 4 * kBlocks) cols[i % kAhead] = value_cols<D>(*cur, vb, i + kAhead);
+      if (ks < 3) {
+#pragma unroll
+        for (int r = 8 * ((ks + 1) % 2) + d * kPer, n = 0; n < kPer; ++r, ++n) s[(ks + 1) / 2][r] = weight(s[(ks + 1) / 2][r]);
+        if (d == kBlocks - 1) p = b_operand(s[(ks + 1) / 2], (ks + 1) % 2);
       }
-      const bf8 p = b_operand(s[ks / 2], ks % 2);
-#pragma unroll
-      for (int d = 0; d < D / 32; ++d) o[d] = mfma(tr_frag<2 * D>(cur->v, vb, 16 * ks, d), p, o[d]);
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
   copy(&tiles[part][0], part);
   for (int t = 0; t < n_tiles; t += 2 * PARTS) {   // two tiles a turn: the buffers' addresses are constants
