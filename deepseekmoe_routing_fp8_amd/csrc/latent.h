@@ -235,4 +235,39 @@ __device__ __forceinline__ void store4(void* base, int64_t at, bool bf16, float 
   }
 }
 
+// Writes a wave's 32 rows of N columns, held as results whose columns are the rows (lane
+// l: row l % 32), to rows first.. of a matrix, `n` of them. The rows pass through LDS
+// (`area`: 32 * N * 4 bytes of the wave's own), so that they go out whole, 16 bytes a lane:
+// stored from the registers, 8 bytes a lane and row, they took longer than the products of
+// a 512-token sequence.
+template <int N, typename T>
+__device__ __forceinline__ void store_rows_as(uint8_t* area, const f16v* v, float factor, T* first, int64_t stride,
+                                              int n, int lane) {
+  constexpr int W = N * (int)sizeof(T), kChunks = W / 16;
+  const int row = lane & 31, hh = lane >> 5;
+#pragma unroll
+  for (int d = 0; d < N / 32; ++d)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = v[d][4 * i] * factor, b = v[d][4 * i + 1] * factor;
+      const float c = v[d][4 * i + 2] * factor, e = v[d][4 * i + 3] * factor;
+      if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<uint2*>(area + tile_off<W>(row, 4 * d + i) + 8 * hh) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, e));
+      else
+        *reinterpret_cast<float4*>(area + tile_off<W>(row, 8 * d + 2 * i + hh)) = make_float4(a, b, c, e);
+    }
+#pragma unroll
+  for (int j = 0; j < 32 * kChunks / kWave; ++j) {
+    const int r = (j * kWave + lane) / kChunks, c = lane % kChunks;
+    const u4 x = *reinterpret_cast<const u4*>(area + tile_off<W>(r, c));
+    if (r < n) *reinterpret_cast<u4*>(reinterpret_cast<uint8_t*>(first + r * stride) + c * 16) = x;
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_rows(uint8_t* area, const f16v* v, float factor, void* base, int64_t first,
+                                           int64_t stride, int n, bool bf16, int lane) {
+  if (bf16) store_rows_as<N>(area, v, factor, static_cast<uint16_t*>(base) + first, stride, n, lane);
+  else store_rows_as<N>(area, v, factor, static_cast<float*>(base) + first, stride, n, lane);
+}
+
 }  // namespace moe

@@ -247,23 +247,15 @@ __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_kv_kernel(const Ba
     if (t + 1 < n_tiles) turn(tile1, tile2, tile0, t + 1);
     if (t + 2 < n_tiles) turn(tile2, tile0, tile1, t + 2);
   }
-  if (key >= sp.nk) return;
-  const int64_t at = ((sp.k0 + key) * a.H + h) * 2 * D + 4 * hh;
-#pragma unroll
-  for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      store4(a.dkv, at + 32 * d + 8 * i, a.bf16, dk[d][4 * i] * a.scale, dk[d][4 * i + 1] * a.scale,
-             dk[d][4 * i + 2] * a.scale, dk[d][4 * i + 3] * a.scale);
-      store4(a.dkv, at + D + 32 * d + 8 * i, a.bf16, dv[d][4 * i], dv[d][4 * i + 1], dv[d][4 * i + 2],
-             dv[d][4 * i + 3]);
-    }
-  float* rp = a.dkr_part + ((int64_t)h * a.Tk + sp.k0 + key) * kRope + 4 * hh;
-#pragma unroll
-  for (int d = 0; d < kRope / 32; ++d)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      store4(rp, 32 * d + 8 * i, false, dr[d][4 * i], dr[d][4 * i + 1], dr[d][4 * i + 2], dr[d][4 * i + 3]);
+  copies_done_barrier();   // every wave is done with the tiles
+  if (w0 >= sp.nk) return;
+  uint8_t* area = reinterpret_cast<uint8_t*>(wave < 2 ? &tile0 : &tile1) + (wave & 1) * 32 * D * 4;
+  static_assert(2 * 32 * D * 4 <= sizeof(tile0), "rows of two waves");
+  const int64_t at = ((sp.k0 + w0) * a.H + h) * 2 * D, stride = (int64_t)a.H * 2 * D;
+  store_rows<D>(area, dk, a.scale, a.dkv, at, stride, sp.nk - w0, a.bf16, lane);
+  store_rows<D>(area, dv, 1.0f, a.dkv, at + D, stride, sp.nk - w0, a.bf16, lane);
+  store_rows<kRope>(area, dr, 1.0f, a.dkr_part, ((int64_t)h * a.Tk + sp.k0 + w0) * kRope, kRope, sp.nk - w0, false,
+                    lane);
 }
 
 // dk_rope[t] = scale * sum of the heads' parts in head order, for tokens of a sequence.
@@ -442,22 +434,22 @@ __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_q_kernel(const Bac
     if (t + 1 < n_tiles) turn(tile1, tile2, tile0, t + 1);
     if (t + 2 < n_tiles) turn(tile2, tile0, tile1, t + 2);
   }
-  if (row >= sp.nq) return;
+  copies_done_barrier();   // every wave is done with the tiles
+  if (w0 >= sp.nq) return;
   off = half_sum(off);
-  if (hh == 0) {
+  if (row < sp.nq && hh == 0) {
     a.lse2[sc] = lse2;
     a.delta[sc] = delta + off;
   }
-  const int64_t at = ((sp.q0 + row) * a.H + h) * (D + kRope) + 4 * hh;
 #pragma unroll
   for (int d = 0; d < kBlocks; ++d)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float v[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = (dq[d][4 * i + e] - off * pk[d][4 * i + e]) * a.scale;
-      store4(a.dq, at + 32 * d + 8 * i, a.bf16, v[0], v[1], v[2], v[3]);
-    }
+    for (int r = 0; r < 16; ++r) dq[d][r] -= off * pk[d][r];
+  uint8_t* area = reinterpret_cast<uint8_t*>(wave < 2 ? &tile0 : &tile1) + (wave & 1) * 32 * D * 4;
+  static_assert(2 * 32 * D * 4 <= sizeof(tile0), "rows of two waves");
+  const int64_t at = ((sp.q0 + w0) * a.H + h) * (D + kRope), stride = (int64_t)a.H * (D + kRope);
+  store_rows<D>(area, dq, a.scale, a.dq, at, stride, sp.nq - w0, a.bf16, lane);
+  store_rows<kRope>(area, dq + D / 32, a.scale, a.dq, at + D, stride, sp.nq - w0, a.bf16, lane);
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }

@@ -206,28 +206,25 @@ __global__ __launch_bounds__(kFWaves* PARTS* kWave, 2) void expanded_kernel(cons
       ml[kWave] = l;
     }
     copies_done_barrier();
-    if (part == 1) return;
-    const float m1 = ml[0], top = fmaxf(m, m1), base = top == kNegInf ? 0.0f : top;
-    const float f0 = __builtin_amdgcn_exp2f(m - base), f1 = __builtin_amdgcn_exp2f(m1 - base);
-    m = top;
-    l = l * f0 + ml[kWave] * f1;
+    if (part == 0) {
+      const float m1 = ml[0], top = fmaxf(m, m1), base = top == kNegInf ? 0.0f : top;
+      const float f0 = __builtin_amdgcn_exp2f(m - base), f1 = __builtin_amdgcn_exp2f(m1 - base);
+      m = top;
+      l = l * f0 + ml[kWave] * f1;
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-      const f4 v = x[i * kWave];
+      for (int i = 0; i < D / 8; ++i) {
+        const f4 v = x[i * kWave];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i / 4][4 * (i % 4) + e] = o[i / 4][4 * (i % 4) + e] * f0 + v[e] * f1;
+        for (int e = 0; e < 4; ++e) o[i / 4][4 * (i % 4) + e] = o[i / 4][4 * (i % 4) + e] * f0 + v[e] * f1;
+      }
     }
   }
-  if (!live) return;
+  copies_done_barrier();   // every wave is done with the tiles (and the joined parts)
+  if (w0 >= nq || (PARTS == 2 && part == 1)) return;
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-  const int64_t at = ((tq0 + row) * a.H + h) * D + 4 * hh;
-#pragma unroll
-  for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      store4(a.out, at + 32 * d + 8 * i, a.out_bf16, o[d][4 * i] * inv, o[d][4 * i + 1] * inv,
-             o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv);
-  if (hh == 0) a.lse[(int64_t)h * a.Tq + tq0 + row] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : kNegInf;
+  uint8_t* area = reinterpret_cast<uint8_t*>(tiles) + wave * 32 * D * 4;
+  store_rows<D>(area, o, inv, a.out, ((tq0 + w0) * a.H + h) * D, (int64_t)a.H * D, nq - w0, a.out_bf16, lane);
+  if (live && hh == 0) a.lse[(int64_t)h * a.Tq + tq0 + row] = l > 0.0f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : kNegInf;
 }
 
 // A CU holds two workgroups of one part or one of two. With fewer than kFewItems (head,
