@@ -109,19 +109,7 @@ __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_kv_kernel(const Ba
   const int key = w0 + col;
   const int ahead = sp.nk - sp.nq;                // query i sees keys j <= i + ahead when causal
 
-  bf8 kf[kSteps], vf[D / 16];
-  {
-    const int64_t kc = sp.k0 + min(key, sp.nk - 1);
-    const uint16_t* kp = a.kv + (kc * a.H + h) * 2 * D + 8 * hh;
-    const uint16_t* rp = a.kr + kc * kRope + 8 * hh;
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s) {
-      kf[s] = *reinterpret_cast<const bf8*>(kp + 16 * s);
-      vf[s] = *reinterpret_cast<const bf8*>(kp + D + 16 * s);
-    }
-#pragma unroll
-    for (int s = 0; s < kRope / 16; ++s) kf[D / 16 + s] = *reinterpret_cast<const bf8*>(rp + 16 * s);
-  }
+  bf8 kf[kSteps], vf[D / 16];   // the wave's keys and values as operands
   f16v dk[D / 32], dr[kRope / 32], dv[D / 32];
 #pragma unroll
   for (int d = 0; d < D / 32; ++d) dk[d] = dv[d] = zero16();
@@ -234,18 +222,47 @@ __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_kv_kernel(const Ba
     hide(t, 1, s1, d1);
     sums(cur, 1, s1, d1, next, 1);
   };
-  copy(tile0, 0);
+  // The wave's keys and values come through the first two tiles (64 keys each), beside the
+  // first queries: read from memory as operands, a lane at a time, every line would be
+  // fetched several times.
+  {
+    const int kv0 = st.tile * kBRows, stride = a.H * 4 * D;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int64_t k0 = sp.k0 + kv0 + 64 * j;
+      const int n = min(64, sp.nk - kv0 - 64 * j);
+      const auto kv = buffer_of(a.kv + (k0 * a.H + h) * 2 * D, (int64_t)max(n, 0) * stride);
+      const auto kr = buffer_of(a.kr + k0 * kRope, (int64_t)max(n, 0) * 2 * kRope);
+      QTile<D>& t = j == 0 ? tile0 : tile1;
+      tile_copy<2 * D, 64, kBWaves>(kv, stride, 0, t.q, wave, lane);
+      tile_copy<2 * kRope, 64, kBWaves>(kr, 2 * kRope, 0, t.r, wave, lane);
+      tile_copy<2 * D, 64, kBWaves>(kv, stride, 2 * D, t.g, wave, lane);
+    }
+  }
+  copy(tile2, 0);
   copies_done_barrier();
-  copy(tile1, 1);
+  {
+    const QTile<D>& t = wave < 2 ? tile0 : tile1;
+    const int r0 = 32 * (wave & 1);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      kf[i] = row_frag<2 * D>(t.q, qb, r0, i);
+      vf[i] = row_frag<2 * D>(t.g, qb, r0, i);
+    }
+#pragma unroll
+    for (int i = 0; i < kRope / 16; ++i) kf[D / 16 + i] = row_frag<2 * kRope>(t.r, rb, r0, i);
+  }
+  copies_done_barrier();
+  copy(tile0, 1);
   if (n_tiles > 0) {
-    ahead_rows(tile0, 0);
-    scores(tile0, 0, s0, d0, tile0, 0, s0, d0, true);
-    ahead_rows(tile0, 1);
+    ahead_rows(tile2, 0);
+    scores(tile2, 0, s0, d0, tile2, 0, s0, d0, true);
+    ahead_rows(tile2, 1);
   }
   for (int t = 0; t < n_tiles; t += 3) {
-    turn(tile0, tile1, tile2, t);
-    if (t + 1 < n_tiles) turn(tile1, tile2, tile0, t + 1);
-    if (t + 2 < n_tiles) turn(tile2, tile0, tile1, t + 2);
+    turn(tile2, tile0, tile1, t);
+    if (t + 1 < n_tiles) turn(tile0, tile1, tile2, t + 1);
+    if (t + 2 < n_tiles) turn(tile1, tile2, tile0, t + 2);
   }
   copies_done_barrier();   // every wave is done with the tiles
   if (w0 >= sp.nk) return;
@@ -293,6 +310,7 @@ template <int D>
 __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_q_kernel(const BackwardArgs a) {
   constexpr int kSteps = (D + kRope) / 16, kBlocks = (D + kRope) / 32;
   __shared__ KTile<D> tile0, tile1, tile2;
+  __shared__ float delta_of[kBWaves][32];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, hh = lane >> 5;
   const int64_t id = list_item(a.q_per_xcd);
@@ -307,25 +325,10 @@ __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_q_kernel(const Bac
   const int wg_limit = a.causal ? min(sp.nk, min(wg0 + kBRows, sp.nq) + ahead) : sp.nk;
   const int n_tiles = max(0, (wg_limit + kBTile - 1) / kBTile);
 
-  bf8 qf[kSteps], gf[D / 16];
+  bf8 qf[kSteps], gf[D / 16];   // the wave's queries and output gradients as operands
   const int64_t rc = sp.q0 + min(row, sp.nq - 1), sc = (int64_t)h * a.Tq + rc;
   float lse2 = a.lse[sc] * kLog2e, delta = 0.0f;
   if (lse2 == kNegInf) lse2 = -kNegInf;   // a row that sees nothing: every weight 0
-  {
-    const uint16_t* qp = a.q + (rc * a.H + h) * (D + kRope) + 8 * hh;
-    const uint16_t* gp = a.dout + (rc * a.H + h) * D + 8 * hh;
-    const uint16_t* op = a.out + (rc * a.H + h) * D + 8 * hh;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) qf[s] = *reinterpret_cast<const bf8*>(qp + 16 * s);
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s) {
-      gf[s] = *reinterpret_cast<const bf8*>(gp + 16 * s);
-      const bf8 o = *reinterpret_cast<const bf8*>(op + 16 * s);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) delta = fmaf((float)gf[s][e], (float)o[e], delta);
-    }
-    delta = half_sum(delta);
-  }
   f16v dq[kBlocks], pk[kBlocks];
 #pragma unroll
   for (int d = 0; d < kBlocks; ++d) dq[d] = pk[d] = zero16();
@@ -421,18 +424,66 @@ __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_q_kernel(const Bac
     hide(t, 1, s1, d1);
     sums(cur, 1, s1, d1, next, 1);
   };
-  copy(tile0, 0);
+  // The wave's queries and output gradients come through the first two tiles (64 rows each),
+  // beside the first keys: read from memory as operands, a lane at a time, every line would
+  // be fetched several times. The outputs are read in whole rows for D.
+  constexpr int kChunks = D / 8, kReads = 32 * kChunks / kWave;   // 16-byte chunks of an output row
+  bf8 ov[kReads];
+#pragma unroll
+  for (int j = 0; j < kReads; ++j) {
+    const int r = (j * kWave + lane) / kChunks, c = lane % kChunks;
+    ov[j] = *reinterpret_cast<const bf8*>(a.out + ((sp.q0 + min(w0 + r, sp.nq - 1)) * a.H + h) * D + 8 * c);
+  }
+  {
+    const int qs = a.H * 2 * (D + kRope), gs = a.H * 2 * D;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int64_t r0 = sp.q0 + wg0 + 64 * j;
+      const int n = max(min(64, sp.nq - wg0 - 64 * j), 0);
+      const auto q = buffer_of(a.q + (r0 * a.H + h) * (D + kRope), (int64_t)n * qs);
+      const auto g = buffer_of(a.dout + (r0 * a.H + h) * D, (int64_t)n * gs);
+      KTile<D>& t = j == 0 ? tile0 : tile1;
+      tile_copy<2 * D, 64, kBWaves>(q, qs, 0, t.k, wave, lane);
+      tile_copy<2 * kRope, 64, kBWaves>(q, qs, 2 * D, t.r, wave, lane);
+      tile_copy<2 * D, 64, kBWaves>(g, gs, 0, t.v, wave, lane);
+    }
+  }
+  copy(tile2, 0);
   copies_done_barrier();
-  copy(tile1, 1);
+  {
+    const KTile<D>& t = wave < 2 ? tile0 : tile1;
+    const int r0 = 32 * (wave & 1);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      qf[i] = row_frag<2 * D>(t.k, kb, r0, i);
+      gf[i] = row_frag<2 * D>(t.v, kb, r0, i);
+    }
+#pragma unroll
+    for (int i = 0; i < kRope / 16; ++i) qf[D / 16 + i] = row_frag<2 * kRope>(t.r, rb, r0, i);
+#pragma unroll
+    for (int j = 0; j < kReads; ++j) {
+      const int r = (j * kWave + lane) / kChunks;
+      const bf8 g = *reinterpret_cast<const bf8*>(t.v + tile_off<2 * D>(r0 + r, lane % kChunks));
+      float sum = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fmaf((float)g[e], (float)ov[j][e], sum);
+#pragma unroll
+      for (int o = kChunks / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+      if (lane % kChunks == 0) delta_of[wave][r] = sum;
+    }
+    delta = delta_of[wave][col];
+  }
+  copies_done_barrier();
+  copy(tile0, 1);
   if (n_tiles > 0) {
-    ahead_rows(tile0, 0);
-    scores(tile0, 0, s0, d0, tile0, 0, s0, d0, true);
-    ahead_rows(tile0, 1);
+    ahead_rows(tile2, 0);
+    scores(tile2, 0, s0, d0, tile2, 0, s0, d0, true);
+    ahead_rows(tile2, 1);
   }
   for (int t = 0; t < n_tiles; t += 3) {
-    turn(tile0, tile1, tile2, t);
-    if (t + 1 < n_tiles) turn(tile1, tile2, tile0, t + 1);
-    if (t + 2 < n_tiles) turn(tile2, tile0, tile1, t + 2);
+    turn(tile2, tile0, tile1, t);
+    if (t + 1 < n_tiles) turn(tile0, tile1, tile2, t + 1);
+    if (t + 2 < n_tiles) turn(tile1, tile2, tile0, t + 2);
   }
   copies_done_barrier();   // every wave is done with the tiles
   if (w0 >= sp.nq) return;
