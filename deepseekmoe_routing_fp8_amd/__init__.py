@@ -639,7 +639,7 @@ def _device_of(t, name: str) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise MoEError(f"{name} must be a device tensor")
     dev = t.get_device()
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise MoEError(f"{name} is on device {dev}, the current one is {torch.cuda.current_device()}")
     return dev
 
@@ -683,13 +683,21 @@ def moe_latent_cache_row_bytes(cfg: moe_latent_config) -> int:
     return int(_lib.moe_latent_cache_row_bytes(ctypes.byref(cfg)))
 
 
+_row_bytes = {}   # (latent, rope) -> bytes of an E4M3 cache row
+
+
 def _cache_args(cfg, cache, dev: int):
     """Address, pages and page size of a cache [n_pages, page_size, row]: uint8 rows of
     moe_latent_cache_row_bytes bytes, or bf16 rows for a bf16 cache."""
     n_pages, page, _ = _dims(cache, 3, "cache")
+    R, W = cfg.latent, cfg.rope
     if cfg.cache_kind == MOE_CACHE_BF16:
-        return _ptr(cache, torch.bfloat16, (n_pages, page, cfg.latent + cfg.rope), dev, "cache"), n_pages, page
-    row = moe_latent_cache_row_bytes(cfg)
+        return _ptr(cache, torch.bfloat16, (n_pages, page, R + W), dev, "cache"), n_pages, page
+    row = _row_bytes.get((R, W))
+    if row is None:
+        row = moe_latent_cache_row_bytes(cfg)
+        if row > 0:   # a valid configuration
+            _row_bytes[R, W] = row
     return _ptr(cache, torch.uint8, (n_pages, page, row), dev, "cache"), n_pages, page
 
 
@@ -700,11 +708,9 @@ def moe_latent_cache_write(cfg: moe_latent_config, x: torch.Tensor, slots: torch
     offset; negative: skipped; distinct). Returns cache."""
     dev = _device_of(x, "x")
     T, W = _dims(x, 2, "x")
-    if W != cfg.latent + cfg.rope:
-        raise MoEError(f"x must have {cfg.latent + cfg.rope} columns, got {W}")
     row, col = x.stride()
-    if col != 1:
-        raise MoEError("the columns of x must be contiguous")
+    if W != cfg.latent + cfg.rope or col != 1:
+        raise MoEError(f"x must have {cfg.latent + cfg.rope} contiguous columns, got {W}")
     ptr, n_pages, page = _cache_args(cfg, cache, dev)
     _check(_lib.moe_latent_cache_write(
         ctypes.byref(cfg), T, x.data_ptr(), _xdtype(x), row if T > 1 else W,

@@ -57,8 +57,11 @@ __global__ __launch_bounds__(256) void cache_write_kernel(const T* __restrict__ 
 }
 
 // A workgroup reads kReadRows output rows: their cache rows are looked up once, then all
-// threads copy 16-byte output pieces.
-constexpr int kReadRows = 16;
+// threads copy 16-byte output pieces, kBatch of a thread in flight together. The output
+// goes past the caches (it is read next by a product over all of it). 60000 E4M3 rows whose
+// lines are in no cache: 36.5 us with 16 rows and plain stores, 32.4 so (32 rows; 35.0
+// with 48, 38.9 with 64).
+constexpr int kReadRows = 32, kReadBatch = 3;
 
 template <int R, bool FP8>
 __global__ __launch_bounds__(256) void cache_read_kernel(const uint8_t* __restrict__ cache, int64_t n_pages,
@@ -87,26 +90,36 @@ __global__ __launch_bounds__(256) void cache_read_kernel(const uint8_t* __restri
     row_of[threadIdx.x] = at;
   }
   __syncthreads();
-  constexpr int kPieces = (R + kRope) / 8;
-  for (int i = threadIdx.x; i < kReadRows * kPieces; i += 256) {
-    const int rr = i / kPieces, p = i % kPieces;
-    if (r0 + rr >= n) break;
-    u4 v = {0, 0, 0, 0};
-    if (row_of[rr] >= 0) {
+  constexpr int kPieces = (R + kRope) / 8, kStep = 256 * kReadBatch;
+  const int n_pieces = (int)min((int64_t)kReadRows, n - r0) * kPieces;
+  for (int i0 = threadIdx.x; i0 < n_pieces; i0 += kStep) {
+    u4 v[kReadBatch];
+    float s[kReadBatch];
+#pragma unroll
+    for (int k = 0; k < kReadBatch; ++k) {
+      const int i = i0 + 256 * k, rr = min(i / kPieces, kReadRows - 1), p = i % kPieces;
+      v[k] = u4{0, 0, 0, 0};
+      s[k] = 1.0f;
+      if (i >= n_pieces || row_of[rr] < 0) continue;
       const uint8_t* row = cache + row_of[rr] * cache_row_bytes(R, FP8);
-      if constexpr (FP8) {
-        if (p < R / 8) {
-          const uint2 q = *reinterpret_cast<const uint2*>(row + p * 8);
-          const float s = *reinterpret_cast<const float*>(row + R + 2 * kRope + 4 * (p / 16));
-          v = unpack_fp8(q, s);
-        } else {
-          v = *reinterpret_cast<const u4*>(row + R + (p - R / 8) * 16);
-        }
+      if (!FP8) {
+        v[k] = *reinterpret_cast<const u4*>(row + p * 16);
+      } else if (p < R / 8) {
+        const uint2 q = *reinterpret_cast<const uint2*>(row + p * 8);
+        v[k][0] = q.x;
+        v[k][1] = q.y;
+        s[k] = *reinterpret_cast<const float*>(row + R + 2 * kRope + 4 * (p / 16));
       } else {
-        v = *reinterpret_cast<const u4*>(row + p * 16);
+        v[k] = *reinterpret_cast<const u4*>(row + R + (p - R / 8) * 16);
       }
     }
-    *reinterpret_cast<u4*>(out + (r0 + rr) * (R + kRope) + p * 8) = v;
+#pragma unroll
+    for (int k = 0; k < kReadBatch; ++k) {
+      const int i = i0 + 256 * k, rr = i / kPieces, p = i % kPieces;
+      if (i >= n_pieces) break;
+      if (FP8 && p < R / 8) v[k] = unpack_fp8(make_uint2(v[k][0], v[k][1]), s[k]);
+      __builtin_nontemporal_store(v[k], reinterpret_cast<u4*>(out + (r0 + rr) * (R + kRope) + p * 8));
+    }
   }
 }
 
