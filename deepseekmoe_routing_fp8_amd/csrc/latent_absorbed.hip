@@ -92,6 +92,8 @@ template <int R>
 struct __attribute__((aligned(16))) CodeTile {
   uint8_t row[kTok][fp8_row_bytes(R)];
 };
+template <>
+struct CodeTile<0> {};   // of a bf16 cache
 
 // Buffers of a workgroup. bf16: NT tiles, the copies NT - 1 ahead. E4M3: two tiles, and the
 // codes of NC tiles, copied NC ahead of their conversion. QL steps of the query operands
@@ -104,7 +106,7 @@ struct Lds {
   static constexpr int kAhead = FP8 ? NC + 1 : NT - 1;   // tiles between a copy and its products
   static constexpr int kCopies = FP8 ? kRows : 2 * kRows;   // a wave's copies for a tile
   LatentTile<R> tile[NT];
-  CodeTile<FP8 ? R : 16> code[FP8 ? NC : 1];
+  CodeTile<FP8 ? R : 0> code[FP8 ? NC : 1];
   bf8 q[kAWaves][QL > 0 ? QL : 1][kWave];
   int wsum[kAWaves], found[2];   // find_range
 };
@@ -118,6 +120,7 @@ template <int R>
 __device__ __forceinline__ void copy_rows(const AbsorbedArgs& a, LatentTile<R>* t, int slots, int l0, int wave,
                                           int lane) {
   constexpr int kBytes = cache_row_bytes(R, false);
+  asm volatile("" : "+v"(lane));   // the lane's offsets are formed here each time, not kept in registers
 #pragma unroll
   for (int j = 0; j < kRows; ++j) {
     const int slot = __builtin_amdgcn_readlane(slots, l0 + j);
@@ -151,6 +154,7 @@ __device__ __forceinline__ void copy_codes(const AbsorbedArgs& a, CodeTile<R>* t
 // The wave's rows of a code tile as bf16.
 template <int R>
 __device__ __forceinline__ void convert_codes(const CodeTile<R>* g, LatentTile<R>* t, int wave, int lane) {
+  asm volatile("" : "+v"(lane));   // (as in copy_rows)
   constexpr int kChunks = R / 16, kSide = kWave / kChunks;   // rows side by side
 #pragma unroll
   for (int j = 0; j < kRows; j += kSide) {
@@ -330,7 +334,7 @@ __global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedAr
     };
     int batch = t0, slots = slots_at(page_at(t0), t0), pages = page_at(t0 + kBatch);
     // copies of tile t (past t1: of nothing); t goes up by one from call to call
-    auto copy = [&](LatentTile<R>* to, CodeTile<FP8 ? R : 16>* codes, int t) __attribute__((always_inline)) {
+    auto copy = [&](LatentTile<R>* to, CodeTile<FP8 ? R : 0>* codes, int t) __attribute__((always_inline)) {
       if (t - batch == kBatch) {
         batch = t;
         slots = slots_at(pages, t);
@@ -357,7 +361,7 @@ __global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedAr
     // One tile. `far` and `codes` are written by copies while `cur` is read, `next` by the
     // conversion: the pointers are declared not to alias, or the reads would wait.
     auto step = [&](const LatentTile<R>* __restrict__ cur, LatentTile<R>* __restrict__ next,
-                    LatentTile<R>* __restrict__ far, CodeTile<FP8 ? R : 16>* __restrict__ codes,
+                    LatentTile<R>* __restrict__ far, CodeTile<FP8 ? R : 0>* __restrict__ codes,
                     int t) __attribute__((always_inline)) {
       if constexpr (FP8) {
         convert_codes<R>(codes, next, wave, lane);
