@@ -829,4 +829,5 @@ def moe_latent_attn_expanded_backward(cfg: moe_latent_config, q: torch.Tensor, k
     return dq, dkv, dk_rope
 
 
+from .latent import LatentAttention  # noqa: E402,F401
 from .layer import MoELayer  # noqa: E402,F401

@@ -1,0 +1,154 @@
+"""Latent-attention driver: a paged cache with its page tables, and the two forms of the
+attention over it through the C entry points.
+
+A token brings its normalised latent vector and rotary key, [c | k_r], and its queries
+[q_n | q_r] a head (the projections before them, the norm and the rotation are the
+caller's). ``w_uk`` and ``w_uv`` expand a latent vector to each head's key part and value.
+
+* ``prefill`` writes a chunk's rows to the cache, reads the sequences' whole contexts back,
+  expands them by one product with [w_uk | w_uv] and runs the expanded form.
+* ``decode`` writes one or a few tokens a sequence and runs the absorbed form: w_uk is folded
+  into the queries and w_uv into the output, so the cached rows are attended to as they are.
+* ``attend_train`` / ``backward`` are the expanded form and its gradients for a training
+  step, where nothing is cached.
+"""
+from __future__ import annotations
+
+import math
+from typing import Sequence
+
+import torch
+
+from . import (make_latent_config, moe_latent_attn_absorbed, moe_latent_attn_absorbed_workspace_bytes,
+               moe_latent_attn_expanded, moe_latent_attn_expanded_backward, moe_latent_cache_read,
+               moe_latent_cache_row_bytes, moe_latent_cache_write)
+
+
+class LatentAttention:
+    """The attention of one layer on one GPU, with a cache for ``max_seqs`` sequences over a
+    pool of ``n_pages`` pages of ``page_size`` rows. Pages are taken as sequences grow and
+    returned by ``release``."""
+
+    def __init__(self, n_heads: int, w_uk: torch.Tensor, w_uv: torch.Tensor, rope: int = 64, cache: str = "fp8",
+                 n_pages: int = 1, page_size: int = 64, max_seqs: int = 1, scale: float = None):
+        """``w_uk`` [n_heads, latent, nope] and ``w_uv`` [n_heads, latent, v_dim], bf16."""
+        H, R, D = w_uk.shape
+        self.cfg = make_latent_config(n_heads, latent=R, rope=rope, nope=D, v_dim=w_uv.shape[2], cache=cache)
+        if H != n_heads or w_uv.shape[:2] != (H, R):
+            raise ValueError("w_uk and w_uv must be [n_heads, latent, width]")
+        self.dev = w_uk.device
+        self.scale = 1.0 / math.sqrt(D + rope) if scale is None else scale
+        # [R, H, nope + v_dim]: one product expands a latent row to every head's key and value
+        self.w_kv = torch.cat([w_uk, w_uv], 2).transpose(0, 1).contiguous().reshape(R, -1)
+        # folded: queries [T, nope] x [nope, R] and outputs [T, R] x [R, v_dim] a head
+        self.w_q = w_uk.transpose(1, 2).contiguous()
+        self.w_o = w_uv.contiguous()
+        width = R + rope if cache == "bf16" else moe_latent_cache_row_bytes(self.cfg)
+        self.cache = torch.zeros((n_pages, page_size, width), device=self.dev,
+                                 dtype=torch.bfloat16 if cache == "bf16" else torch.uint8)
+        self.page_size = page_size
+        self.free = list(range(n_pages - 1, -1, -1))
+        self.pages = [[] for _ in range(max_seqs)]   # host copy of each sequence's pages
+        self.lens = [0] * max_seqs
+        self.ws = None
+
+    def _check(self, seqs: Sequence[int], counts: Sequence[int], rows: torch.Tensor, q: torch.Tensor):
+        """Before any page is taken: a refused call leaves the sequences as they were."""
+        c, T = self.cfg, sum(counts)
+        if len(seqs) != len(counts) or len(set(seqs)) != len(seqs) or not len(seqs) or min(counts) < 0:
+            raise ValueError("seqs must be distinct, with a count of zero or more each")
+        if min(seqs) < 0 or max(seqs) >= len(self.pages):
+            raise ValueError(f"seqs must be in 0..{len(self.pages) - 1}")
+        if rows.dtype not in (torch.bfloat16, torch.float32) or rows.numel() != T * (c.latent + c.rope):
+            raise ValueError(f"rows must hold {T} x {c.latent + c.rope} bf16 or f32 values")
+        if q.dtype != torch.bfloat16 or q.numel() != T * c.n_heads * (c.nope + c.rope):
+            raise ValueError(f"q must hold {T} x {c.n_heads} x {c.nope + c.rope} bf16 values")
+
+    # -- pages ---------------------------------------------------------------------
+    def _grow(self, seqs: Sequence[int], counts: Sequence[int]) -> torch.Tensor:
+        """Takes pages for ``counts`` more rows of each sequence; -> their cache rows, int32."""
+        P, slots = self.page_size, []
+        need = sum(max(0, -(-(self.lens[b] + n) // P) - len(self.pages[b])) for b, n in zip(seqs, counts))
+        if need > len(self.free):
+            raise RuntimeError(f"cache full: {need} pages needed, {len(self.free)} free")
+        for b, n in zip(seqs, counts):
+            while len(self.pages[b]) * P < self.lens[b] + n:
+                self.pages[b].append(self.free.pop())
+            slots += [self.pages[b][p // P] * P + p % P for p in range(self.lens[b], self.lens[b] + n)]
+            self.lens[b] += n
+        return torch.tensor(slots, dtype=torch.int32, device=self.dev)
+
+    def _table(self, seqs: Sequence[int]) -> torch.Tensor:
+        width = max(1, max(len(self.pages[b]) for b in seqs))
+        return torch.tensor([self.pages[b] + [0] * (width - len(self.pages[b])) for b in seqs], dtype=torch.int32,
+                            device=self.dev)
+
+    def release(self, seq: int):
+        """Ends a sequence: its pages return to the pool."""
+        self.free += reversed(self.pages[seq])
+        self.pages[seq], self.lens[seq] = [], 0
+
+    def _offsets(self, counts: Sequence[int]) -> torch.Tensor:
+        at = [0]
+        for n in counts:
+            at.append(at[-1] + n)
+        return torch.tensor(at, dtype=torch.int32, device=self.dev)
+
+    # -- serving -------------------------------------------------------------------
+    def prefill(self, seqs: Sequence[int], counts: Sequence[int], rows: torch.Tensor, q: torch.Tensor) -> torch.Tensor:
+        """``counts[i]`` new tokens of sequence ``seqs[i]``, packed: rows [T, latent + rope]
+        (bf16 or f32), q [T, n_heads, nope + rope] bf16 -> [T, n_heads, v_dim] bf16. The new
+        tokens attend to their sequences' earlier context as well."""
+        c = self.cfg
+        self._check(seqs, counts, rows, q)
+        moe_latent_cache_write(c, rows, self._grow(seqs, counts), self.cache)
+        lens = [self.lens[b] for b in seqs]
+        cu_k = self._offsets(lens)
+        ctx = moe_latent_cache_read(c, self.cache, self._table(seqs), cu_k, n_out=sum(lens))
+        kv = torch.matmul(ctx[:, :c.latent].contiguous(), self.w_kv).reshape(-1, c.n_heads, c.nope + c.v_dim)
+        out, _ = moe_latent_attn_expanded(c, q, kv, ctx[:, c.latent:].contiguous(), self._offsets(counts), cu_k,
+                                          self.scale)
+        return out
+
+    def decode(self, seqs: Sequence[int], rows: torch.Tensor, q: torch.Tensor) -> torch.Tensor:
+        """The next tokens of each sequence, the same number of each: rows
+        [B, Sq, latent + rope], q [B, Sq, n_heads, nope + rope] bf16 -> [B, Sq, n_heads, v_dim]
+        bf16."""
+        c = self.cfg
+        B, Sq, H, _ = q.shape
+        self._check(seqs, [Sq] * B, rows, q)
+        moe_latent_cache_write(c, rows.reshape(B * Sq, -1), self._grow(seqs, [Sq] * B), self.cache)
+        lens = torch.tensor([self.lens[b] for b in seqs], dtype=torch.int32, device=self.dev)
+        heads = q.reshape(B * Sq, H, -1).transpose(0, 1)
+        folded = torch.bmm(heads[:, :, :c.nope].contiguous(), self.w_q)   # [H, B * Sq, latent]
+        qa = torch.cat([folded.transpose(0, 1), q[..., c.nope:].reshape(B * Sq, H, -1)], 2)
+        need = moe_latent_attn_absorbed_workspace_bytes(c, B, Sq)
+        if self.ws is None or self.ws.numel() < need:
+            self.ws = torch.empty((need,), dtype=torch.uint8, device=self.dev)
+        lat, _ = moe_latent_attn_absorbed(c, qa.reshape(B, Sq, H, -1), self.cache, self._table(seqs), lens, self.scale,
+                                          ws=self.ws)
+        out = torch.bmm(lat.reshape(B * Sq, H, -1).transpose(0, 1).contiguous(), self.w_o)
+        return out.transpose(0, 1).reshape(B, Sq, H, c.v_dim)
+
+    # -- training ------------------------------------------------------------------
+    def attend_train(self, counts: Sequence[int], rows: torch.Tensor, q: torch.Tensor) -> torch.Tensor:
+        """Packed documents of ``counts`` tokens, causal, nothing cached: rows
+        [T, latent + rope], q [T, n_heads, nope + rope], both bf16 -> [T, n_heads, v_dim]
+        bf16. What ``backward`` needs is kept."""
+        c = self.cfg
+        cu = self._offsets(counts)
+        lat, k_rope = rows[:, :c.latent].contiguous(), rows[:, c.latent:].contiguous()
+        kv = torch.matmul(lat, self.w_kv).reshape(-1, c.n_heads, c.nope + c.v_dim)
+        out, lse = moe_latent_attn_expanded(c, q, kv, k_rope, cu, cu, self.scale)
+        self.kept = (q, kv, k_rope, cu, lat, out, lse)
+        return out
+
+    def backward(self, dout: torch.Tensor):
+        """Gradients of the last ``attend_train`` for dout [T, n_heads, v_dim] bf16 ->
+        (dq, drows, dw_kv): of q, of rows and of the expansion [latent, n_heads, nope + v_dim]."""
+        c = self.cfg
+        q, kv, k_rope, cu, lat, out, lse = self.kept
+        dq, dkv, dk_rope = moe_latent_attn_expanded_backward(c, q, kv, k_rope, cu, cu, self.scale, out, lse, dout)
+        flat = dkv.reshape(dkv.shape[0], -1)
+        drows = torch.cat([torch.matmul(flat, self.w_kv.t().contiguous()), dk_rope], 1)
+        return dq, drows, torch.matmul(lat.t().contiguous(), flat).reshape(c.latent, c.n_heads, -1)

@@ -543,6 +543,9 @@ moe_status moe_grouped_ffn_fp8_backward(
  *   expanded   per-head keys [k_n | k_r] and values v formed from c (prefill, training),
  *              with its backward.
  * Sizes that are built: latent 256 or 512, rope 64, (nope, v_dim) = (64, 64) or (128, 128).
+ * NaN and infinities stay within their sequence: rows past a length, other pages and other
+ * sequences never reach a result. Inside a sequence they may also reach queries that the
+ * causal rule hides them from, since a hidden key enters the value product with weight 0.
  */
 typedef enum moe_cache_kind {
   MOE_CACHE_BF16 = 0, /* a row is latent + rope bf16 values                              */
@@ -612,7 +615,8 @@ moe_status moe_latent_cache_read(const moe_latent_config* cfg, const void* cache
  *   ws       moe_latent_attn_absorbed_workspace_bytes(cfg, B, Sq) bytes, 16-byte aligned
  * Errors: invalid config, Sq outside 1..64, B < 0, B > 65535, page_size < 1, other sizes
  * < 0 or max_pages * page_size >= 2^31, scale not positive and finite (SHAPE); dtype; NULL
- * pointers; workspace; misaligned q, cache, out or ws (UNSUPPORTED).
+ * pointers; workspace; misaligned q, cache, out or ws, or a table whose 32-row tiles are too
+ * many for a 32-bit count (B * max_pages * page_size / 32 > 0x7fff0000) (UNSUPPORTED).
  */
 size_t moe_latent_attn_absorbed_workspace_bytes(const moe_latent_config* cfg, int64_t B, int32_t Sq);
 moe_status moe_latent_attn_absorbed(const moe_latent_config* cfg, int64_t B, int32_t Sq, const uint16_t* q,

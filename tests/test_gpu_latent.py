@@ -242,6 +242,27 @@ def test_absorbed(lib, H, Sq, width, kind, page, lens):
     assert torch.equal(lse32, lse) and torch.equal(out32.to(torch.bfloat16), out)
 
 
+@pytest.mark.parametrize("H,Sq,width,kind,B", [(16, 1, 512, "fp8", 64), (16, 1, 512, "fp8", 65), (8, 2, 256, "bf16", 200),
+                                               (128, 1, 512, "bf16", 130), (4, 1, 512, "fp8", 513),
+                                               (16, 1, 256, "fp8", 1300)])
+def test_absorbed_many_sequences(lib, H, Sq, width, kind, B):
+    """More sequences than lanes, than threads of a workgroup and than workgroups; lengths
+    from none up, with runs of empty sequences and some long ones."""
+    say(f"absorbed H={H} Sq={Sq} latent={width} {kind} B={B}")
+    rng = np.random.default_rng(B)
+    cfg = lib.make_latent_config(H, latent=width, cache=kind)
+    lens = rng.integers(0, 100, B)
+    lens[rng.random(B) < 0.3] = 0
+    lens[B // 3: B // 3 + 12] = 0
+    lens[[0, 7, B - 1]] = 0, 900, 400
+    cache, table, ctx = paged(rng, lib, cfg, kind, width, [int(n) for n in lens], 16)
+    q = rand(rng, B, Sq, H, width + 64)
+    out, lse = lib.moe_latent_attn_absorbed(cfg, bf(q), cache, table, dev(lens.astype(np.int32)), 0.07)
+    ref, rl, mag = latent.absorbed(q, ctx, width, np.float32(0.07))
+    assert_within(host(out), ref, out_bound(ref, mag), "out")
+    assert_lse(host(lse), rl)
+
+
 def test_absorbed_lengths_and_pages_out_of_range(lib):
     """Lengths past the table are clamped, negative ones are empty; a page outside the pool
     reads as zero rows."""
