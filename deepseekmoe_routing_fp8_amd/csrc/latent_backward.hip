@@ -97,6 +97,7 @@ template <int D>
 __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_kv_kernel(const BackwardArgs a) {
   constexpr int kSteps = (D + kRope) / 16;
   __shared__ QTile<D> tile0, tile1, tile2;
+  __shared__ __attribute__((aligned(256))) uint8_t more[2][64 * 2 * D];   // keys and values of waves 2 and 3
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, hh = lane >> 5;
   const int64_t id = list_item(a.k_per_xcd);
@@ -222,38 +223,36 @@ __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_kv_kernel(const Ba
     hide(t, 1, s1, d1);
     sums(cur, 1, s1, d1, next, 1);
   };
-  // The wave's keys and values come through the first two tiles (64 keys each), beside the
-  // first queries: read from memory as operands, a lane at a time, every line would be
-  // fetched several times.
+  // The keys and values of waves 0 and 1 come through tile1, those of the others through
+  // `more`, beside the first two tiles: read from memory as operands, a lane at a time,
+  // every line would be fetched several times (the rotary keys are, a line a row: there is no
+  // room for them).
   {
     const int kv0 = st.tile * kBRows, stride = a.H * 4 * D;
+    const uint16_t* kr = a.kr + (sp.k0 + min(key, sp.nk - 1)) * kRope + 8 * hh;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int64_t k0 = sp.k0 + kv0 + 64 * j;
-      const int n = min(64, sp.nk - kv0 - 64 * j);
-      const auto kv = buffer_of(a.kv + (k0 * a.H + h) * 2 * D, (int64_t)max(n, 0) * stride);
-      const auto kr = buffer_of(a.kr + k0 * kRope, (int64_t)max(n, 0) * 2 * kRope);
-      QTile<D>& t = j == 0 ? tile0 : tile1;
-      tile_copy<2 * D, 64, kBWaves>(kv, stride, 0, t.q, wave, lane);
-      tile_copy<2 * kRope, 64, kBWaves>(kr, 2 * kRope, 0, t.r, wave, lane);
-      tile_copy<2 * D, 64, kBWaves>(kv, stride, 2 * D, t.g, wave, lane);
+      const int n = max(min(64, sp.nk - kv0 - 64 * j), 0);
+      const auto kv = buffer_of(a.kv + (k0 * a.H + h) * 2 * D, (int64_t)n * stride);
+      tile_copy<2 * D, 64, kBWaves>(kv, stride, 0, j == 0 ? tile1.q : more[0], wave, lane);
+      tile_copy<2 * D, 64, kBWaves>(kv, stride, 2 * D, j == 0 ? tile1.g : more[1], wave, lane);
     }
+    copy(tile2, 0);
+    copy(tile0, 1);
+#pragma unroll
+    for (int i = 0; i < kRope / 16; ++i) kf[D / 16 + i] = *reinterpret_cast<const bf8*>(kr + 16 * i);
   }
-  copy(tile2, 0);
   copies_done_barrier();
   {
-    const QTile<D>& t = wave < 2 ? tile0 : tile1;
+    const uint8_t *k = wave < 2 ? tile1.q : more[0], *v = wave < 2 ? tile1.g : more[1];
     const int r0 = 32 * (wave & 1);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
-      kf[i] = row_frag<2 * D>(t.q, qb, r0, i);
-      vf[i] = row_frag<2 * D>(t.g, qb, r0, i);
+      kf[i] = row_frag<2 * D>(k, qb, r0, i);
+      vf[i] = row_frag<2 * D>(v, qb, r0, i);
     }
-#pragma unroll
-    for (int i = 0; i < kRope / 16; ++i) kf[D / 16 + i] = row_frag<2 * kRope>(t.r, rb, r0, i);
   }
-  copies_done_barrier();
-  copy(tile0, 1);
   if (n_tiles > 0) {
     ahead_rows(tile2, 0);
     scores(tile2, 0, s0, d0, tile2, 0, s0, d0, true);
@@ -306,11 +305,22 @@ __device__ __forceinline__ void copy_k(const BackwardArgs& a, KTile<D>* t, int64
   tile_copy<2 * D, kBTile, kBWaves>(kv, stride, 2 * D, t->v, wave, lane);
 }
 
+// The sum over N = 8 or 16 adjacent lanes, in each of them (data-parallel moves within rows of
+// 16 lanes: exchanges by 1 and 2, then halves and the row mirrored).
+template <int N>
+__device__ __forceinline__ float chunk_sum(float v) {
+  auto add = [](float x, int y) { return x + __int_as_float(y); };
+  v = add(v, __builtin_amdgcn_mov_dpp(__float_as_int(v), 0xB1, 0xF, 0xF, true));
+  v = add(v, __builtin_amdgcn_mov_dpp(__float_as_int(v), 0x4E, 0xF, 0xF, true));
+  v = add(v, __builtin_amdgcn_mov_dpp(__float_as_int(v), 0x141, 0xF, 0xF, true));
+  if constexpr (N == 16) v = add(v, __builtin_amdgcn_mov_dpp(__float_as_int(v), 0x140, 0xF, 0xF, true));
+  return v;
+}
+
 template <int D>
 __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_q_kernel(const BackwardArgs a) {
   constexpr int kSteps = (D + kRope) / 16, kBlocks = (D + kRope) / 32;
-  __shared__ KTile<D> tile0, tile1, tile2;
-  __shared__ float delta_of[kBWaves][32];
+  __shared__ KTile<D> tile0, tile1, tile2, more;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, hh = lane >> 5;
   const int64_t id = list_item(a.q_per_xcd);
@@ -327,8 +337,7 @@ __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_q_kernel(const Bac
 
   bf8 qf[kSteps], gf[D / 16];   // the wave's queries and output gradients as operands
   const int64_t rc = sp.q0 + min(row, sp.nq - 1), sc = (int64_t)h * a.Tq + rc;
-  float lse2 = a.lse[sc] * kLog2e, delta = 0.0f;
-  if (lse2 == kNegInf) lse2 = -kNegInf;   // a row that sees nothing: every weight 0
+  float lse2, delta;
   f16v dq[kBlocks], pk[kBlocks];
 #pragma unroll
   for (int d = 0; d < kBlocks; ++d) dq[d] = pk[d] = zero16();
@@ -424,16 +433,9 @@ __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_q_kernel(const Bac
     hide(t, 1, s1, d1);
     sums(cur, 1, s1, d1, next, 1);
   };
-  // The wave's queries and output gradients come through the first two tiles (64 rows each),
-  // beside the first keys: read from memory as operands, a lane at a time, every line would
-  // be fetched several times. The outputs are read in whole rows for D.
-  constexpr int kChunks = D / 8, kReads = 32 * kChunks / kWave;   // 16-byte chunks of an output row
-  bf8 ov[kReads];
-#pragma unroll
-  for (int j = 0; j < kReads; ++j) {
-    const int r = (j * kWave + lane) / kChunks, c = lane % kChunks;
-    ov[j] = *reinterpret_cast<const bf8*>(a.out + ((sp.q0 + min(w0 + r, sp.nq - 1)) * a.H + h) * D + 8 * c);
-  }
+  // The queries and output gradients of waves 0 and 1 come through tile1, those of the others
+  // through `more`, beside the first two tiles: read from memory as operands, a lane at a time,
+  // every line would be fetched several times. The outputs are read in whole rows for D.
   {
     const int qs = a.H * 2 * (D + kRope), gs = a.H * 2 * D;
 #pragma unroll
@@ -442,16 +444,26 @@ __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_q_kernel(const Bac
       const int n = max(min(64, sp.nq - wg0 - 64 * j), 0);
       const auto q = buffer_of(a.q + (r0 * a.H + h) * (D + kRope), (int64_t)n * qs);
       const auto g = buffer_of(a.dout + (r0 * a.H + h) * D, (int64_t)n * gs);
-      KTile<D>& t = j == 0 ? tile0 : tile1;
+      KTile<D>& t = j == 0 ? tile1 : more;
       tile_copy<2 * D, 64, kBWaves>(q, qs, 0, t.k, wave, lane);
       tile_copy<2 * kRope, 64, kBWaves>(q, qs, 2 * D, t.r, wave, lane);
       tile_copy<2 * D, 64, kBWaves>(g, gs, 0, t.v, wave, lane);
     }
   }
   copy(tile2, 0);
+  copy(tile0, 1);
+  constexpr int kChunks = D / 8, kReads = 32 * kChunks / kWave;   // 16-byte chunks of an output row
+  bf8 ov[kReads];
+#pragma unroll
+  for (int j = 0; j < kReads; ++j) {
+    const int r = (j * kWave + lane) / kChunks, c = lane % kChunks;
+    ov[j] = *reinterpret_cast<const bf8*>(a.out + ((sp.q0 + min(w0 + r, sp.nq - 1)) * a.H + h) * D + 8 * c);
+  }
+  lse2 = a.lse[sc] * kLog2e;
   copies_done_barrier();
+  if (lse2 == kNegInf) lse2 = -kNegInf;   // a row that sees nothing: every weight 0
   {
-    const KTile<D>& t = wave < 2 ? tile0 : tile1;
+    KTile<D>& t = wave < 2 ? tile1 : more;
     const int r0 = 32 * (wave & 1);
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
@@ -460,21 +472,26 @@ __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_q_kernel(const Bac
     }
 #pragma unroll
     for (int i = 0; i < kRope / 16; ++i) qf[D / 16 + i] = row_frag<2 * kRope>(t.r, rb, r0, i);
+    float sum[kReads];
 #pragma unroll
     for (int j = 0; j < kReads; ++j) {
       const int r = (j * kWave + lane) / kChunks;
       const bf8 g = *reinterpret_cast<const bf8*>(t.v + tile_off<2 * D>(r0 + r, lane % kChunks));
-      float sum = 0.0f;
+      sum[j] = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum = fmaf((float)g[e], (float)ov[j][e], sum);
-#pragma unroll
-      for (int o = kChunks / 2; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
-      if (lane % kChunks == 0) delta_of[wave][r] = sum;
+      for (int e = 0; e < 8; ++e) sum[j] = fmaf((float)g[e], (float)ov[j][e], sum[j]);
     }
-    delta = delta_of[wave][col];
+#pragma unroll
+    for (int j = 0; j < kReads; ++j) sum[j] = chunk_sum<kChunks>(sum[j]);
+    // from the lanes of a row to the lanes of its column, through the first of the wave's
+    // own rows (32 floats), which are read
+    asm volatile("" ::: "memory");
+    float* own = reinterpret_cast<float*>(t.v + r0 * 2 * D);
+#pragma unroll
+    for (int j = 0; j < kReads; ++j)
+      if (lane % kChunks == 0) own[(j * kWave + lane) / kChunks] = sum[j];
+    delta = own[col];
   }
-  copies_done_barrier();
-  copy(tile0, 1);
   if (n_tiles > 0) {
     ahead_rows(tile2, 0);
     scores(tile2, 0, s0, d0, tile2, 0, s0, d0, true);
