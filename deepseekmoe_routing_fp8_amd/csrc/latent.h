@@ -239,7 +239,8 @@ __device__ __forceinline__ void store4(void* base, int64_t at, bool bf16, float 
 // l: row l % 32), to rows first.. of a matrix, `n` of them. The rows pass through LDS
 // (`area`: 32 * N * 4 bytes of the wave's own), so that they go out whole, 16 bytes a lane:
 // stored from the registers, 8 bytes a lane and row, they took longer than the products of
-// a 512-token sequence.
+// a 512-token sequence. They go past the caches, whose room is the keys' and values' (a
+// chunked prefill over 32 heads, 2200 new tokens on 15000 to 25000: 151 us against 160).
 template <int N, typename T>
 __device__ __forceinline__ void store_rows_as(uint8_t* area, const f16v* v, float factor, T* first, int64_t stride,
                                               int n, int lane) {
@@ -260,7 +261,7 @@ __device__ __forceinline__ void store_rows_as(uint8_t* area, const f16v* v, floa
   for (int j = 0; j < 32 * kChunks / kWave; ++j) {
     const int r = (j * kWave + lane) / kChunks, c = lane % kChunks;
     const u4 x = *reinterpret_cast<const u4*>(area + tile_off<W>(r, c));
-    if (r < n) *reinterpret_cast<u4*>(reinterpret_cast<uint8_t*>(first + r * stride) + c * 16) = x;
+    if (r < n) __builtin_nontemporal_store(x, reinterpret_cast<u4*>(reinterpret_cast<uint8_t*>(first + r * stride) + c * 16));
   }
 }
 template <int N>

@@ -282,7 +282,7 @@ __global__ __launch_bounds__(256) void rope_sum_kernel(const float* __restrict__
   if (t >= Tk || t < cu_k[0] || t >= cu_k[B]) return;
   f4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
-  for (int h = 0; h < H; ++h) sum += *reinterpret_cast<const f4*>(part + (int64_t)h * Tk * kRope + i);
+  for (int h = 0; h < H; ++h) sum += __builtin_nontemporal_load(reinterpret_cast<const f4*>(part + (int64_t)h * Tk * kRope + i));
   store4(out, i, bf16, sum[0] * scale, sum[1] * scale, sum[2] * scale, sum[3] * scale);
 }
 
