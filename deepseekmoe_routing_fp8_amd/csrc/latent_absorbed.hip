@@ -30,7 +30,7 @@ constexpr int kTok = 32;        // cached rows a tile
 constexpr int kAWaves = 8;
 constexpr int kAThreads = kAWaves * kWave;
 constexpr int kGroups = 256;    // workgroups: one a CU
-constexpr int kMinTiles = 2;    // tiles a range holds at least
+constexpr int kMinTiles = 2;    // tiles a range holds at least (777 rows: 14.8 us with 1 or 2, 15.7 with 3)
 constexpr int kAhead = 3;         // depth steps whose rows are read ahead
 constexpr float kSlack = 8.0f;  // how far (log2) a score may pass the reference of its row
 
@@ -59,7 +59,7 @@ __device__ __forceinline__ int length_of(const AbsorbedArgs& a, int b) {
 // many as the workgroups need; for few long sequences more, since the parts of a block of
 // query rows are joined one after another by the waves of one workgroup: n tiles a block
 // cost n / g for the join and g for the range, least at g ~ sqrt(n) (one sequence of 20000
-// rows, 16 heads: 39 us at 3 tiles, 32 at 7).
+// rows, 16 heads: 38.5 us at 3 tiles a range, 29.5 at 8, 34.0 at 16).
 __device__ __forceinline__ int64_t range_tiles(const AbsorbedArgs& a, int64_t total) {
   const int64_t even = (total * a.blocks + kGroups - 1) / kGroups;
   const int64_t few = (int64_t)sqrtf((float)total / (float)a.B * 0.1f);
@@ -511,15 +511,13 @@ __global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedAr
 }
 
 // Joins the partial results of a block of query rows, or writes the empty result of a
-// sequence without rows. A workgroup takes 16 query rows and 64 columns; its waves take
-// every fourth partial result each, then 16 columns each of the four waves' sums.
-constexpr int kJoinWaves = 4;
-
-template <int R, int WQ>
-__global__ __launch_bounds__(kJoinWaves* kWave) void absorbed_join_kernel(const AbsorbedArgs a) {
+// sequence without rows. A workgroup takes 16 query rows and COLS blocks of 16 columns; each of
+// its WAVES waves takes every WAVES-th partial result, and the waves' sums meet in LDS.
+template <int R, int WQ, int COLS, int WAVES>
+__global__ __launch_bounds__(WAVES* kWave) void absorbed_join_kernel(const AbsorbedArgs a) {
   constexpr int kQRows = 16 * WQ;
-  __shared__ f4 osum[kJoinWaves][4][kWave];
-  __shared__ float msum[kJoinWaves][16], lsum[kJoinWaves][16];
+  __shared__ f4 osum[WAVES][COLS][kWave];
+  __shared__ float msum[WAVES][16], lsum[WAVES][16];
   const int unit = blockIdx.x;
   const int wq = unit % WQ, blk = unit / WQ % a.blocks, b = unit / WQ / a.blocks;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, grp = lane >> 4;
@@ -531,37 +529,40 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void absorbed_join_kernel(const 
   if (g0 == g1 || blk * kQRows + wq * 16 >= M) return;   // one range had all of it, or no query row
   auto part = [&](int64_t g) { return a.part + (g * 2 + (s0 <= g * per ? 0 : 1)) * part_floats(R, kQRows); };
   float m = kNegInf, l = 0.0f;
-  f4 o[4] = {};
-#pragma unroll 2
-  for (int64_t g = g0 + wave; g <= g1; g += kJoinWaves) {
+  f4 o[COLS] = {};
+#pragma unroll (8 / COLS)
+  for (int64_t g = g0 + wave; g <= g1; g += WAVES) {
     const float* p = part(g);
     const float mg = p[kQRows * R + wq * 16 + col], lg = p[kQRows * (R + 1) + wq * 16 + col];
-    const f4* og = reinterpret_cast<const f4*>(p) + (wq * (R / 16) + blockIdx.y * 4) * kWave + lane;
-    const f4 v[4] = {og[0], og[kWave], og[2 * kWave], og[3 * kWave]};
+    const f4* og = reinterpret_cast<const f4*>(p) + (wq * (R / 16) + blockIdx.y * COLS) * kWave + lane;
+    f4 v[COLS];
+#pragma unroll
+    for (int d = 0; d < COLS; ++d) v[d] = og[d * kWave];
     const float top = fmaxf(m, mg), base = top == kNegInf ? 0.0f : top;
     const float f0 = __builtin_amdgcn_exp2f(m - base), f1 = __builtin_amdgcn_exp2f(mg - base);
     m = top;
     l = l * f0 + lg * f1;
 #pragma unroll
-    for (int d = 0; d < 4; ++d)
+    for (int d = 0; d < COLS; ++d)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[d][e] = fmaf(f1, v[d][e], o[d][e] * f0);
   }
 #pragma unroll
-  for (int d = 0; d < 4; ++d) osum[wave][d][lane] = o[d];
+  for (int d = 0; d < COLS; ++d) osum[wave][d][lane] = o[d];
   if (grp == 0) {
     msum[wave][col] = m;
     lsum[wave][col] = l;
   }
   __syncthreads();
+  if (wave >= COLS) return;   // a block of columns each
   m = kNegInf;
 #pragma unroll
-  for (int w = 0; w < kJoinWaves; ++w) m = fmaxf(m, msum[w][col]);
+  for (int w = 0; w < WAVES; ++w) m = fmaxf(m, msum[w][col]);
   const float top = m == kNegInf ? 0.0f : m;
   l = 0.0f;
   f4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int w = 0; w < kJoinWaves; ++w) {
+  for (int w = 0; w < WAVES; ++w) {
     const float f = __builtin_amdgcn_exp2f(msum[w][col] - top);
     l = fmaf(f, lsum[w][col], l);
     const f4 v = osum[w][wave][lane];
@@ -570,7 +571,7 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void absorbed_join_kernel(const 
   }
   if (row >= M) return;
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-  const int d = blockIdx.y * 4 + wave;
+  const int d = blockIdx.y * COLS + wave;
   store4(a.out, ((int64_t)b * M + row) * R + 16 * d + 4 * grp, a.out_bf16, sum[0] * inv, sum[1] * inv, sum[2] * inv,
          sum[3] * inv);
   if (d == 0 && grp == 0)
@@ -585,13 +586,23 @@ __global__ __launch_bounds__(kJoinWaves* kWave) void absorbed_join_kernel(const 
 int query_rows(int M) { return M > 32 ? 128 : M > 16 ? 64 : 32; }
 size_t first_bytes(int64_t B) { return ((size_t)(B + 2) * 8 + 255) / 256 * 256; }
 
+// Few (16 query rows, sequence) units: one block of columns a workgroup and eight waves, since
+// there is little else to hide the loads behind; many: four blocks, whole 4 KB pieces of a
+// partial result at a time. 16 heads, four blocks against one: one sequence of 20000 rows 29.2
+// and 24.8 us, 8 of 4000 (16 units) 26.7 and 25.4, 16 (32) 30.8 and 30.5, 32 (64) 40.8 and 42.4,
+// 64 of 2000 (128) 41.4 and 46.4.
+constexpr int kFewUnits = 32;
+
 template <int R, int WQ>
 void launch_absorbed(const AbsorbedArgs& a, bool fp8, hipStream_t s) {
   constexpr int WD = kAWaves / WQ;
   if (fp8) hipLaunchKernelGGL((absorbed_kernel<R, WQ, WD, true>), dim3(kGroups), dim3(kAThreads), 0, s, a);
   else hipLaunchKernelGGL((absorbed_kernel<R, WQ, WD, false>), dim3(kGroups), dim3(kAThreads), 0, s, a);
-  hipLaunchKernelGGL((absorbed_join_kernel<R, WQ>), dim3((unsigned)(a.B * a.blocks * WQ), R / 64),
-                     dim3(kJoinWaves * kWave), 0, s, a);
+  const int units = a.B * a.blocks * WQ;
+  if (units <= kFewUnits)
+    hipLaunchKernelGGL((absorbed_join_kernel<R, WQ, 1, 8>), dim3((unsigned)units, R / 16), dim3(8 * kWave), 0, s, a);
+  else
+    hipLaunchKernelGGL((absorbed_join_kernel<R, WQ, 4, 4>), dim3((unsigned)units, R / 64), dim3(4 * kWave), 0, s, a);
 }
 
 template <int R>
