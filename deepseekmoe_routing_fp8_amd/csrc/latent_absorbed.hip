@@ -12,7 +12,8 @@
 //
 // The work is the sequences' tiles laid end to end, (sequence, block of query rows, tile),
 // cut into equal ranges for a fixed number of workgroups: ragged lengths balance without
-// the host knowing them. A block of query rows whose tiles fall into several ranges leaves
+// the host knowing them. Before the tiles of each block stand a few units for what it costs
+// to begin and end one. A block of query rows whose tiles fall into several ranges leaves
 // its partial sums (O unnormalised, maximum, sum, all FP32) in the workspace, and a second
 // kernel joins them in range order.
 //
@@ -30,7 +31,7 @@ constexpr int kTok = 32;        // cached rows a tile
 constexpr int kAWaves = 8;
 constexpr int kAThreads = kAWaves * kWave;
 constexpr int kGroups = 256;    // workgroups: one a CU
-constexpr int kMinTiles = 2;    // tiles a range holds at least (777 rows: 14.8 us with 1 or 2, 15.7 with 3)
+constexpr int kMinTiles = 2;    // units a range holds at least (777 rows: 14.8 us with 1 or 2, 15.7 with 3)
 constexpr int kAhead = 3;         // depth steps whose rows are read ahead
 constexpr float kSlack = 8.0f;  // how far (log2) a score may pass the reference of its row
 
@@ -40,7 +41,7 @@ struct AbsorbedArgs {
   const int32_t *table, *lengths;
   void* out;
   float* lse;
-  int64_t* first;      // [B + 2]: tiles before each sequence (one block of query rows); tiles of a range
+  int64_t* first;      // [B + 2]: units before each sequence (one block of query rows); units of a range
   float* part;         // [kGroups][2] partial results
   int64_t n_pages, max_pages;
   int B, Sq, H, page, blocks;   // blocks of query rows a sequence
@@ -55,7 +56,16 @@ __device__ __forceinline__ f4 mfma16(bf8 a, bf8 b, f4 c) {
 __device__ __forceinline__ int length_of(const AbsorbedArgs& a, int b) {
   return (int)min((int64_t)max(a.lengths[b], 0), a.max_pages * a.page);
 }
-// Tiles of a range, for `total` tiles of all sequences (one block of query rows). At least as
+// Units of a (sequence, block of query rows): kLead for its beginning and end, then its tiles.
+// A workgroup's second and third piece cost it 14000 to 25000 clocks beside their tiles, of
+// 3300 (16 heads) to 5300 (128) clocks each; without them, the workgroups that hold ends of
+// sequences finish last (384 query rows, 31 sequences of up to 4097: 211000 clocks where most
+// have 126000). With 0, 2, 4, 5 and 6 the three large cases of 16, 128 and 384 query rows take
+// 136, 133, 130, 129, 129 us; 131, 123, 115, 113, 114; and 112, 100, 90, 85, 85.
+constexpr int kLead = 5;
+__device__ __forceinline__ int units_of(int n_tiles) { return n_tiles > 0 ? n_tiles + kLead : 0; }
+
+// Units of a range, for `total` units of all sequences (one block of query rows). At least as
 // many as the workgroups need; for few long sequences more, since the parts of a block of
 // query rows are joined one after another by the waves of one workgroup: n tiles a block
 // cost n / g for the join and g for the range, least at g ~ sqrt(n) (one sequence of 20000
@@ -203,8 +213,8 @@ __device__ __forceinline__ int range_of(const AbsorbedArgs& a, int64_t total, in
 }
 
 // Where a workgroup's range begins: the sequence that holds its first tile and the number
-// of tiles before that sequence; total: tiles of all sequences (one block of query rows);
-// per: tiles of a range; id: the workgroup's range.
+// of units before that sequence; total: units of all sequences (one block of query rows);
+// per: units of a range; id: the workgroup's range.
 struct Range {
   int b;
   int64_t before, total, per;
@@ -227,7 +237,7 @@ __device__ __forceinline__ int wave_scan(int v, int lane) {
 __device__ __forceinline__ Range find_range(const AbsorbedArgs& a, int* wsum, int* found, int wave, int lane) {
   Range r{-1, 0, 0, 0, 0};
   if (a.B <= kWave) {   // each wave by itself
-    const int n = lane < a.B ? tiles_of(a, lane) : 0;
+    const int n = lane < a.B ? units_of(tiles_of(a, lane)) : 0;
     const int incl = wave_scan(n, lane);
     r.total = __builtin_amdgcn_readlane(incl, kWave - 1);
     r.per = range_tiles(a, r.total);
@@ -250,7 +260,7 @@ __device__ __forceinline__ Range find_range(const AbsorbedArgs& a, int* wsum, in
   // the total first (it fixes the ranges), then the sums, 512 sequences at a time
   const int tid = wave * kWave + lane;
   int sum = 0;
-  for (int b = tid; b < a.B; b += kAThreads) sum += tiles_of(a, b);
+  for (int b = tid; b < a.B; b += kAThreads) sum += units_of(tiles_of(a, b));
   sum = wave_scan(sum, lane);
   if (lane == kWave - 1) wsum[wave] = sum;
   if (tid == 0) found[0] = -1;
@@ -262,7 +272,7 @@ __device__ __forceinline__ Range find_range(const AbsorbedArgs& a, int* wsum, in
   const int64_t start = r.id * r.per;
   int before = 0;
   for (int b0 = 0; b0 < a.B; b0 += kAThreads) {
-    const int b = b0 + tid, n = b < a.B ? tiles_of(a, b) : 0;
+    const int b = b0 + tid, n = b < a.B ? units_of(tiles_of(a, b)) : 0;
     int incl = wave_scan(n, lane);
     __syncthreads();
     if (lane == kWave - 1) wsum[wave] = incl;
@@ -321,15 +331,20 @@ __global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedAr
   const int ct = (latent_off<R>(4 * grp + (col >> 2), (col & 3) >> 1) + ((col & 1) << 3)) ^ ((wd * kFrags & 7) << 5);
   for (int64_t at = start; at < end;) {
     int len = length_of(a, b);
-    int n = (len + kTok - 1) / kTok;
-    while (at >= seq0 + (int64_t)n * a.blocks) {   // the next sequence with tiles
-      seq0 += (int64_t)n * a.blocks;
+    int n = (len + kTok - 1) / kTok, units = units_of(n);
+    while (at >= seq0 + (int64_t)units * a.blocks) {   // the next sequence with tiles
+      seq0 += (int64_t)units * a.blocks;
       ++b;
       len = length_of(a, b);
       n = (len + kTok - 1) / kTok;
+      units = units_of(n);
     }
-    const int blk = (int)((at - seq0) / n), t0 = (int)((at - seq0) % n);
-    const int t1 = (int)min((int64_t)n, t0 + (end - at));
+    const int blk = (int)((at - seq0) / units), u0 = (int)((at - seq0) % units);
+    const int u1 = (int)min((int64_t)units, u0 + (end - at));
+    const int t0 = max(u0 - kLead, 0), t1 = u1 - kLead;
+    const bool first = at == start;
+    at += u1 - u0;
+    if (t1 <= t0) continue;   // the lead only
     const bool whole = t0 == 0 && t1 == n;
     const int row = blk * kQRows + wq * 16 + col;
     const bool busy = blk * kQRows + wq * 16 < M;
@@ -495,7 +510,7 @@ __global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedAr
         }
       } else {
         // lanes side by side: [wq][column block of 16][lane][4]
-        float* p = a.part + ((int64_t)id * 2 + (at == start ? 0 : 1)) * part_floats(R, kQRows);
+        float* p = a.part + ((int64_t)id * 2 + (first ? 0 : 1)) * part_floats(R, kQRows);
 #pragma unroll
         for (int d = 0; d < kFrags; ++d)
           *reinterpret_cast<f4*>(p + ((wq * (R / 16) + wd * kFrags + d) * 64 + lane) * 4) = o[d];
@@ -505,7 +520,6 @@ __global__ __launch_bounds__(kAThreads, 2) void absorbed_kernel(const AbsorbedAr
         }
       }
     }
-    at += t1 - t0;
     copies_done_barrier();   // every wave is done with the buffers before the next block's copies
   }
 }
@@ -523,9 +537,9 @@ __global__ __launch_bounds__(WAVES* kWave) void absorbed_join_kernel(const Absor
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, grp = lane >> 4;
   const int M = a.Sq * a.H, row = blk * kQRows + wq * 16 + col;
   const int64_t n = a.first[b + 1] - a.first[b];
-  const int64_t s0 = a.first[b] * a.blocks + blk * n, s1 = s0 + n;
+  const int64_t s0 = a.first[b] * a.blocks + blk * n, s1 = s0 + n;   // units
   const int64_t per = a.first[a.B + 1];
-  const int64_t g0 = s0 / per, g1 = n > 0 ? (s1 - 1) / per : g0 - 1;
+  const int64_t g0 = (s0 + kLead) / per, g1 = n > 0 ? (s1 - 1) / per : g0 - 1;   // ranges with tiles
   if (g0 == g1 || blk * kQRows + wq * 16 >= M) return;   // one range had all of it, or no query row
   auto part = [&](int64_t g) { return a.part + (g * 2 + (s0 <= g * per ? 0 : 1)) * part_floats(R, kQRows); };
   float m = kNegInf, l = 0.0f;
@@ -649,8 +663,8 @@ extern "C" moe_status moe_latent_attn_absorbed(const moe_latent_config* cfg, int
                        reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + first_bytes(B)), n_pages, max_pages,
                        (int)B, Sq, cfg->n_heads, page_size, (M + query_rows(M) - 1) / query_rows(M), scale * kLog2e,
                        ot == MOE_BF16};
-  if ((int64_t)a.B * a.blocks * 8 > 0x7fffffff || max_pages * page_size / kTok * B > 0x7fff0000)
-    return MOE_ERR_UNSUPPORTED;   // 32-bit counts of tiles
+  if ((int64_t)a.B * a.blocks * 8 > 0x7fffffff || (max_pages * page_size / kTok + 1 + kLead) * B > 0x7fff0000)
+    return MOE_ERR_UNSUPPORTED;   // 32-bit counts of units
   const bool fp8 = cfg->cache_kind == MOE_CACHE_FP8;
   if (cfg->latent == 512) launch_rows<512>(a, fp8, as_stream(stream));
   else launch_rows<256>(a, fp8, as_stream(stream));
