@@ -20,7 +20,11 @@
 // A wave holds its operands and sums in about 400 registers, one wave a SIMD, so the wave
 // itself has to keep both pipes busy: the scores of the next 32 rows are formed while the
 // exponentials of the current ones are taken. Tiles come through a ring of three, copied
-// two ahead.
+// two ahead. 4096 tokens in two documents, 128 heads of 128, causal: 0.90 to 1.0 ms for dQ, 0.82
+// to 0.94 ms for dK and dV. A tile of the first kernel takes 4440 clocks, of which the products
+// need 2820; without the weights 3930, without the copies 3990, without the reads of rows
+// 4120, without all of these 3390. A workgroup's 17 tiles (on average) stand beside 16000
+// clocks of loading its operands and storing its results, since nothing else fits the CU.
 #include "latent.h"
 
 namespace moe {
@@ -274,7 +278,8 @@ __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_kv_kernel(const Ba
                     lane);
 }
 
-// dk_rope[t] = scale * sum of the heads' parts in head order, for tokens of a sequence.
+// dk_rope[t] = scale * sum of the heads' parts in head order, for tokens of a sequence. Bound
+// by the parts' bytes (128 heads, 4096 tokens: 134 MB in 24 us, 5.6 TB/s).
 __global__ __launch_bounds__(256) void rope_sum_kernel(const float* __restrict__ part,
                                                        const int32_t* __restrict__ cu_k, int B, int64_t Tk,
                                                        int H, float scale, void* __restrict__ out, int bf16) {
