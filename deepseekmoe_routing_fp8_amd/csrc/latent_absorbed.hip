@@ -39,7 +39,7 @@ constexpr int kTok = 32;        // cached rows a tile
 constexpr int kAWaves = 8;
 constexpr int kAThreads = kAWaves * kWave;
 constexpr int kGroups = 256;    // workgroups: one a CU
-constexpr int kMinTiles = 2;    // units a range holds at least (777 rows: 14.8 us with 1 or 2, 15.7 with 3)
+constexpr int kMinTiles = 2;    // units a range holds at least (777 rows: the same time with 1, 2 and 3)
 constexpr int kAhead = 3;         // depth steps whose rows are read ahead
 constexpr float kSlack = 8.0f;  // how far (log2) a score may pass the reference of its row
 
@@ -77,7 +77,7 @@ __device__ __forceinline__ int units_of(int n_tiles) { return n_tiles > 0 ? n_ti
 // many as the workgroups need; for few long sequences more, since the parts of a block of
 // query rows are joined one after another by the waves of one workgroup: n tiles a block
 // cost n / g for the join and g for the range, least at g ~ sqrt(n) (one sequence of 20000
-// rows, 16 heads: 38.5 us at 3 tiles a range, 29.5 at 8, 34.0 at 16).
+// rows, 16 heads: 27.0 us at 3 units a range, 24.6 at 8, 31.4 at 16).
 __device__ __forceinline__ int64_t range_tiles(const AbsorbedArgs& a, int64_t total) {
   const int64_t even = (total * a.blocks + kGroups - 1) / kGroups;
   const int64_t few = (int64_t)sqrtf((float)total / (float)a.B * 0.1f);
@@ -605,8 +605,8 @@ __global__ __launch_bounds__(WAVES* kWave) void absorbed_join_kernel(const Absor
 // Query rows of a workgroup: twice as many 16-row groups as the queries fill, up to 8. More
 // groups mean fewer waves that form the same scores, but half of the waves are without rows
 // then and only copy. 64 sequences of 2048 rows, with as many groups as filled, twice and
-// four times as many: 16 heads 39.4, 34.9, 36.0 us (bf16), 42.0, 35.7, 37.8 (E4M3); 32 heads
-// 43.3, 38.8, 40.3 and 46.2, 40.6, 44.5; 64 heads 50.3, 47.8 and 52.5, 51.8.
+// four times as many: 16 heads 40.7, 36.6, 38.5 us (bf16), 44.6, 38.2, 40.9 (E4M3); 32 heads
+// 44.5, 41.9, 43.6 and 48.1, 44.3, 47.0; 64 heads (as filled, twice) 53.4, 50.9 and 55.9, 53.8.
 int query_rows(int M) { return M > 32 ? 128 : M > 16 ? 64 : 32; }
 size_t first_bytes(int64_t B) { return ((size_t)(B + 2) * 8 + 255) / 256 * 256; }
 

@@ -615,8 +615,8 @@ moe_status moe_latent_cache_read(const moe_latent_config* cfg, const void* cache
  *   ws       moe_latent_attn_absorbed_workspace_bytes(cfg, B, Sq) bytes, 16-byte aligned
  * Errors: invalid config, Sq outside 1..64, B < 0, B > 65535, page_size < 1, other sizes
  * < 0 or max_pages * page_size >= 2^31, scale not positive and finite (SHAPE); dtype; NULL
- * pointers; workspace; misaligned q, cache, out or ws, or a table whose 32-row tiles are too
- * many for a 32-bit count (B * max_pages * page_size / 32 > 0x7fff0000) (UNSUPPORTED).
+ * pointers; workspace; misaligned q, cache, out or ws, or tables whose tiles are too many for
+ * a 32-bit count (B * (max_pages * page_size / 32 + 6) > 0x7fff0000) (UNSUPPORTED).
  */
 size_t moe_latent_attn_absorbed_workspace_bytes(const moe_latent_config* cfg, int64_t B, int32_t Sq);
 moe_status moe_latent_attn_absorbed(const moe_latent_config* cfg, int64_t B, int32_t Sq, const uint16_t* q,

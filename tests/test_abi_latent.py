@@ -95,7 +95,7 @@ CHECKS = [
     ("absorbed", dict(table=None), NULL), ("absorbed", dict(cache=None), NULL), ("absorbed", dict(q=odd), UNSUPPORTED),
     ("absorbed", dict(cache=odd), UNSUPPORTED), ("absorbed", dict(ws=odd), UNSUPPORTED),
     ("absorbed", dict(ws=None), WORKSPACE), ("absorbed", dict(ws_bytes=1000), WORKSPACE),
-    ("absorbed", dict(B=0, q=None), OK),
+    ("absorbed", dict(B=0, q=None), OK), ("absorbed", dict(B=65535, max_pages=0x7fffff0, page=16), UNSUPPORTED),
     ("expanded", dict(B=-1), SHAPE), ("expanded", dict(Tq=-1), SHAPE), ("expanded", dict(Tk=1 << 31), SHAPE),
     ("expanded", dict(scale=0.0), SHAPE), ("expanded", dict(ot=9), DTYPE), ("expanded", dict(q=None), NULL),
     ("expanded", dict(kv=None), NULL), ("expanded", dict(kr=None), NULL), ("expanded", dict(cu=None), NULL),
