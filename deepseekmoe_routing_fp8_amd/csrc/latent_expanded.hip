@@ -177,6 +177,9 @@ __global__ __launch_bounds__(kFWaves* PARTS* kWave, 2) void expanded_kernel(cons
 #pragma unroll
     for (int r = 0; r < 8; ++r) s[0][r] = weight(s[0][r]);
     bf8 p = b_operand(s[0], 0);
+    // Of a SIMD's two waves the one that is further in its tile issues first, which keeps them
+    // at different parts of it: 664 us against 697 for 4096 tokens and 128 heads.
+    __builtin_amdgcn_s_setprio(1);
     constexpr int kBlocks = D / 32, kPer = 8 / kBlocks;
 #pragma unroll
     for (int i = 0; i < 4 * kBlocks; ++i) {
@@ -191,6 +194,7 @@ __global__ __launch_bounds__(kFWaves* PARTS* kWave, 2) void expanded_kernel(cons
       }
     }
     __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(0);
   };
   copy(&tiles[part][0], part);
   for (int t = 0; t < n_tiles; t += 2 * PARTS) {   // two tiles a turn: the buffers' addresses are constants
