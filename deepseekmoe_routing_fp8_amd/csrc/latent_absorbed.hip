@@ -25,7 +25,7 @@
 //
 // Few heads are bound by the rows' bytes: 16 heads, 128 sequences, 548000 bf16 rows take
 // 129 us, 4.9 TB/s, what a copy of 2 GiB reaches. 128 heads (64 sequences, 261000 E4M3 rows,
-// 73 GFLOP, 118 us) are bound by no one thing: a tile takes a workgroup 5200 clocks, of
+// 73 GFLOP, 111 us) are bound by no one thing: a tile takes a workgroup 5200 clocks, of
 // which the products need 2200, the LDS reads 2800 (each wave reads the whole tile, for the
 // scores and again for the values) and the conversion and the weights the rest, and the
 // barrier between tiles keeps the waves in step; the partial results (84 MB written and

@@ -7,9 +7,9 @@
 // maxima, sums and O stay in FP32; P's bf16 rounding (relative 2^-8 a term) is that of the
 // inputs. Keys and values reach LDS by direct copies, one tile ahead.
 //
-// Bound by the matrix products and what their wave does between them (60% of the matrix
+// Bound by the matrix products and what their wave does between them (63% of the matrix
 // cycles are used; the clock falls to 1.9 GHz under this load): 4096 tokens, 128 heads of 128,
-// causal, 687 GFLOP in 700 us, 0.98 PFLOP/s; chunks of 300 to 700 tokens on contexts of 1000 to
+// causal, 687 GFLOP in 668 us, 1.03 PFLOP/s; chunks of 300 to 700 tokens on contexts of 1000 to
 // 8000, 32 heads, 114 GFLOP in 160 us, where 480 (head, tile) pairs leave a tenth of the CUs'
 // time unused.
 #include "latent.h"
