@@ -116,10 +116,6 @@ __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_kv_kernel(const Ba
 
   bf8 kf[kSteps], vf[D / 16];   // the wave's keys and values as operands
   f16v dk[D / 32], dr[kRope / 32], dv[D / 32];
-#pragma unroll
-  for (int d = 0; d < D / 32; ++d) dk[d] = dv[d] = zero16();
-#pragma unroll
-  for (int d = 0; d < kRope / 32; ++d) dr[d] = zero16();
   const int qb = row_base<2 * D>(lane), rb = row_base<2 * kRope>(lane);
   const int qt = tr_base<2 * D>(lane), rt = tr_base<2 * kRope>(lane);
 
@@ -247,6 +243,17 @@ __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_kv_kernel(const Ba
 #pragma unroll
     for (int i = 0; i < kRope / 16; ++i) kf[D / 16 + i] = *reinterpret_cast<const bf8*>(kr + 16 * i);
   }
+  __builtin_amdgcn_sched_barrier(0);   // the sums are cleared while the copies arrive (1% of a training step)
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d) {
+    dk[d] = dv[d] = zero16();
+    asm volatile("" : "+a"(dk[d]), "+a"(dv[d]));
+  }
+#pragma unroll
+  for (int d = 0; d < kRope / 32; ++d) {
+    dr[d] = zero16();
+    asm volatile("" : "+a"(dr[d]));
+  }
   copies_done_barrier();
   {
     const uint8_t *k = wave < 2 ? tile1.q : more[0], *v = wave < 2 ? tile1.g : more[1];
@@ -344,8 +351,6 @@ __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_q_kernel(const Bac
   const int64_t rc = sp.q0 + min(row, sp.nq - 1), sc = (int64_t)h * a.Tq + rc;
   float lse2, delta;
   f16v dq[kBlocks], pk[kBlocks];
-#pragma unroll
-  for (int d = 0; d < kBlocks; ++d) dq[d] = pk[d] = zero16();
   float off = 0.0f;   // this lane's part of the row sum of dS
   const int kb = row_base<2 * D>(lane), rb = row_base<2 * kRope>(lane);
   const int kt = tr_base<2 * D>(lane), rt = tr_base<2 * kRope>(lane);
@@ -464,8 +469,15 @@ __global__ __launch_bounds__(kBWaves* kWave, 1) void backward_q_kernel(const Bac
     const int r = (j * kWave + lane) / kChunks, c = lane % kChunks;
     ov[j] = *reinterpret_cast<const bf8*>(a.out + ((sp.q0 + min(w0 + r, sp.nq - 1)) * a.H + h) * D + 8 * c);
   }
-  lse2 = a.lse[sc] * kLog2e;
+  lse2 = a.lse[sc];
+  __builtin_amdgcn_sched_barrier(0);   // (as in the kernel above)
+#pragma unroll
+  for (int d = 0; d < kBlocks; ++d) {
+    dq[d] = pk[d] = zero16();
+    asm volatile("" : "+a"(dq[d]), "+a"(pk[d]));
+  }
   copies_done_barrier();
+  lse2 *= kLog2e;
   if (lse2 == kNegInf) lse2 = -kNegInf;   // a row that sees nothing: every weight 0
   {
     KTile<D>& t = wave < 2 ? tile1 : more;
